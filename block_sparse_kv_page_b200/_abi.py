@@ -24,6 +24,9 @@ SA_SCORE_CENTROID = 1
 SA_OUT_F32 = 0
 SA_OUT_BF16 = 1
 
+SA_KV_BF16 = 0
+SA_KV_E4M3 = 1
+
 SA_BUDGET_TOPK = 0
 SA_BUDGET_RATIO = 1
 SA_BUDGET_TOKENS = 2
@@ -54,6 +57,27 @@ class sa_budget(C.Structure):
         ("bos", C.c_int32),
         ("eos", C.c_int32),
         ("token_budget", C.c_int32),
+    ]
+
+
+class sa_paged_desc(C.Structure):
+    _fields_ = [
+        ("batch", C.c_int32),
+        ("n_kv_heads", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("page_size", C.c_int32),
+        ("n_pages", C.c_int64),
+        ("dtype", C.c_int32),
+        ("max_pages", C.c_int32),
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("page_stride", C.c_int64),
+        ("head_stride", C.c_int64),
+        ("token_stride", C.c_int64),
+        ("k_scale", C.c_void_p),
+        ("v_scale", C.c_void_p),
+        ("page_table", C.c_void_p),
+        ("seq_len", C.c_void_p),
     ]
 
 
@@ -108,6 +132,17 @@ PROTOTYPES = {
     "sparse_attn_decode_static": (C.c_int, [C.POINTER(sa_kv_desc), C.c_void_p, C.c_int32, C.c_int32,
                                             C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p,
                                             C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "sparse_attn_paged_workspace_size": (C.c_size_t, [C.POINTER(sa_paged_desc), C.c_int32]),
+    "sparse_attn_cache_write": (C.c_int, [C.POINTER(sa_paged_desc), C.c_void_p, C.c_void_p, C.c_int64,
+                                          C.c_void_p, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "sparse_attn_cache_read": (C.c_int, [C.POINTER(sa_paged_desc), C.c_int32, C.c_void_p, C.c_void_p,
+                                         C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "sparse_attn_chunk": (C.c_int, [C.POINTER(sa_paged_desc), C.c_void_p, C.c_int64, C.c_int32, C.c_void_p,
+                                    C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_int32,
+                                    C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "sparse_attn_paged_decode": (C.c_int, [C.POINTER(sa_paged_desc), C.c_void_p, C.c_int64, C.c_int32,
+                                           C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_int32,
+                                           C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "sparse_attn_get_device_status": (C.c_int, [C.c_void_p, C.POINTER(C.c_int), C.c_void_p]),
     "sparse_attn_status_string": (C.c_char_p, [C.c_int]),
 }

@@ -28,7 +28,6 @@
 
 namespace sa {
 
-constexpr int kMaxUnits = 65536;
 constexpr size_t kQueueSelect = 64;
 constexpr size_t kQueueDecode = 72;
 constexpr size_t kQueueRoute = 80;
@@ -36,7 +35,6 @@ constexpr size_t kQueueStep = 88;
 constexpr size_t kQueueRouteStep = 96;  // routed decode step: units selected, triggers-published flag
 constexpr int kMaxRouteTiles = 1024;
 constexpr int kMaxRouteList = 1023;
-constexpr size_t kScratch = 256 + 4 * (size_t)kMaxUnits;
 constexpr int kMaxSelectPages = 16384;
 constexpr int kMaxChunkSel = 8192;
 

@@ -1,0 +1,187 @@
+// C-ABI entry points of the paged cache: host-side argument validation and
+// kernel launches (cache_io.cu, paged_attn.cu).
+//
+// Workspace: the layout of the other calls (api.cu): the status word at 0, the
+// unit counters (not used here, left as they are), per-call scratch from
+// kScratch on.
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "paged.h"
+
+namespace sa {
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+sa_status launched(cudaError_t e) {
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return SA_ERR_CUDA;
+  }
+  return SA_OK;
+}
+
+sa_status check_paged(const sa_paged_desc* kv) {
+  if (!kv) return SA_ERR_INVALID;
+  if (kv->batch < 1 || kv->n_kv_heads < 1 || kv->max_pages < 1 || kv->n_pages < 1) return SA_ERR_INVALID;
+  if (kv->dtype != SA_KV_BF16 && kv->dtype != SA_KV_E4M3) return SA_ERR_INVALID;
+  if (kv->head_dim != kHeadDim) return SA_ERR_UNSUPPORTED;
+  if (kv->page_size % 16 != 0 || kv->page_size < 16 || kv->page_size > 256) return SA_ERR_UNSUPPORTED;
+  if (kv->n_pages > 0x7fffffffLL || (long long)kv->max_pages * kv->page_size > 0x7fffffffLL)
+    return SA_ERR_UNSUPPORTED;
+  if (!kv->k || !kv->v || !aligned(kv->k, 16) || !aligned(kv->v, 16)) return SA_ERR_INVALID;
+  const int64_t step = kv->dtype == SA_KV_E4M3 ? 16 : 8;  // elements of 16 bytes
+  if (kv->token_stride < kHeadDim || kv->token_stride % step || kv->head_stride < kHeadDim ||
+      kv->head_stride % step || kv->page_stride < kHeadDim || kv->page_stride % step)
+    return SA_ERR_INVALID;
+  // the tensor maps of the attention kernels take strides below 2^40 bytes
+  const int64_t most = ((int64_t)1 << 40) / (kv->dtype == SA_KV_E4M3 ? 1 : 2);
+  if (kv->token_stride >= most || kv->head_stride >= most || kv->page_stride >= most) return SA_ERR_UNSUPPORTED;
+  if (kv->dtype == SA_KV_E4M3) {
+    if (!kv->k_scale || !kv->v_scale || !aligned(kv->k_scale, 16) || !aligned(kv->v_scale, 16))
+      return SA_ERR_INVALID;
+  } else if (kv->k_scale || kv->v_scale) {
+    return SA_ERR_INVALID;
+  }
+  if (!kv->page_table || !kv->seq_len || !aligned(kv->page_table, 4) || !aligned(kv->seq_len, 4))
+    return SA_ERR_INVALID;
+  return SA_OK;
+}
+
+PagedView paged_view(const sa_paged_desc* kv) {
+  PagedView v{};
+  const int bytes = kv->dtype == SA_KV_E4M3 ? 1 : 2;
+  v.B = kv->batch;
+  v.Hkv = kv->n_kv_heads;
+  v.page_size = kv->page_size;
+  v.max_pages = kv->max_pages;
+  v.n_pages = kv->n_pages;
+  v.e4m3 = kv->dtype == SA_KV_E4M3 ? 1 : 0;
+  v.k = (unsigned char*)kv->k;
+  v.v = (unsigned char*)kv->v;
+  v.page_stride = kv->page_stride * bytes;
+  v.head_stride = kv->head_stride * bytes;
+  v.token_stride = kv->token_stride * bytes;
+  v.k_scale = kv->k_scale;
+  v.v_scale = kv->v_scale;
+  v.table = kv->page_table;
+  v.seq_len = kv->seq_len;
+  return v;
+}
+
+// The status word of an optional workspace.
+sa_status status_word(void* ws, size_t ws_bytes, int** status) {
+  *status = nullptr;
+  if (!ws) return SA_OK;
+  if (!aligned(ws, 256) || ws_bytes < 256) return SA_ERR_WORKSPACE;
+  *status = (int*)ws;
+  return SA_OK;
+}
+
+sa_status check_heads(const sa_paged_desc* kv, int n_q_heads, int* G) {
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads != 0) return SA_ERR_INVALID;
+  *G = n_q_heads / kv->n_kv_heads;
+  if (*G > kMaxGroup) return SA_ERR_UNSUPPORTED;
+  return SA_OK;
+}
+
+sa_status paged_attention(const sa_paged_desc* kv, const void* q, int64_t q_row_stride, int n_q_heads,
+                          const int32_t* row_off, int n_rows, int window, int sinks, float scale, void* out,
+                          int out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  PagedAttnArgs a{};
+  sa_status s = check_paged(kv);
+  if (s != SA_OK) return s;
+  if ((s = check_heads(kv, n_q_heads, &a.G)) != SA_OK) return s;
+  if (!q || !aligned(q, 16) || q_row_stride < (int64_t)n_q_heads * kHeadDim || q_row_stride % 8)
+    return SA_ERR_INVALID;
+  if (n_rows < 0 || window < 0 || sinks < 0 || !std::isfinite(scale)) return SA_ERR_INVALID;
+  if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return SA_ERR_INVALID;
+  if (out_dtype != SA_OUT_F32 && out_dtype != SA_OUT_BF16) return SA_ERR_INVALID;
+  const size_t need = sparse_attn_paged_workspace_size(kv, n_q_heads);
+  if (!ws || !aligned(ws, 256) || ws_bytes < need) return SA_ERR_WORKSPACE;
+  if (n_rows == 0) return SA_OK;
+  a.kv = paged_view(kv);
+  a.q = (const __nv_bfloat16*)q;
+  a.q_row_stride = q_row_stride;
+  a.Hq = n_q_heads;
+  a.row_off = row_off;
+  a.n_rows = n_rows;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale = scale;
+  if (out_dtype == SA_OUT_BF16) a.out_bf16 = (__nv_bfloat16*)out;
+  else a.out = (float*)out;
+  a.lse = lse;
+  a.status = (int*)ws;
+  return launched(launch_paged_attn(a, (cudaStream_t)stream));
+}
+
+}  // namespace
+}  // namespace sa
+
+using namespace sa;
+
+extern "C" {
+
+size_t sparse_attn_paged_workspace_size(const sa_paged_desc* kv, int32_t n_q_heads) {
+  int G;
+  if (check_paged(kv) != SA_OK || check_heads(kv, n_q_heads, &G) != SA_OK) return 0;
+  return kScratch;
+}
+
+sa_status sparse_attn_cache_write(const sa_paged_desc* kv, const void* k_new, const void* v_new,
+                                  int64_t row_stride, const int32_t* row_off, int32_t n_rows, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  sa_status s = check_paged(kv);
+  if (s != SA_OK) return s;
+  CacheWriteArgs a{};
+  if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16)) return SA_ERR_INVALID;
+  if (row_stride < (int64_t)kv->n_kv_heads * kHeadDim || row_stride % 8) return SA_ERR_INVALID;
+  if (!row_off || !aligned(row_off, 4) || n_rows < 0) return SA_ERR_INVALID;
+  if ((s = status_word(ws, ws_bytes, &a.status)) != SA_OK) return s;
+  if (n_rows == 0) return SA_OK;
+  if ((long long)n_rows * kv->n_kv_heads > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
+  a.kv = paged_view(kv);
+  a.k_new = (const __nv_bfloat16*)k_new;
+  a.v_new = (const __nv_bfloat16*)v_new;
+  a.row_stride = row_stride;
+  a.row_off = row_off;
+  a.n_rows = n_rows;
+  return launched(launch_cache_write(a, (cudaStream_t)stream));
+}
+
+sa_status sparse_attn_cache_read(const sa_paged_desc* kv, int32_t first_token, void* k_out, void* v_out,
+                                 int64_t cap_tokens, void* ws, size_t ws_bytes, void* stream) {
+  sa_status s = check_paged(kv);
+  if (s != SA_OK) return s;
+  CacheReadArgs a{};
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || cap_tokens < 1) return SA_ERR_INVALID;
+  if ((s = status_word(ws, ws_bytes, &a.status)) != SA_OK) return s;
+  a.kv = paged_view(kv);
+  a.first_token = first_token;
+  a.k_out = (__nv_bfloat16*)k_out;
+  a.v_out = (__nv_bfloat16*)v_out;
+  a.cap = cap_tokens;
+  return launched(launch_cache_read(a, (cudaStream_t)stream));
+}
+
+sa_status sparse_attn_chunk(const sa_paged_desc* kv, const void* q, int64_t q_row_stride, int32_t n_q_heads,
+                            const int32_t* row_off, int32_t n_rows, int32_t window, int32_t sinks, float scale,
+                            void* out, int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!row_off || !aligned(row_off, 4)) return SA_ERR_INVALID;
+  return paged_attention(kv, q, q_row_stride, n_q_heads, row_off, n_rows, window, sinks, scale, out, out_dtype,
+                         lse, ws, ws_bytes, stream);
+}
+
+sa_status sparse_attn_paged_decode(const sa_paged_desc* kv, const void* q, int64_t q_row_stride,
+                                   int32_t n_q_heads, int32_t window, int32_t sinks, float scale, void* out,
+                                   int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!kv) return SA_ERR_INVALID;
+  return paged_attention(kv, q, q_row_stride, n_q_heads, nullptr, kv->batch, window, sinks, scale, out, out_dtype,
+                         lse, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

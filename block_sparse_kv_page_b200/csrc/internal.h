@@ -11,6 +11,9 @@
 
 namespace sa {
 
+constexpr int kMaxUnits = 65536;                            // unit counters of the workspace
+constexpr size_t kScratch = 256 + 4 * (size_t)kMaxUnits;    // per-call scratch starts here
+
 // Plain copy of the cache view, passed to kernels by value.
 struct KvView {
   int B, Hkv, page_size;      // page_size 0 = variable chunks

@@ -12,7 +12,7 @@ import torch
 
 from . import _abi
 from ._abi import (SA_BUDGET_RATIO, SA_BUDGET_TOKENS, SA_BUDGET_TOPK, SA_SCORE_CENTROID,
-                   SA_SCORE_ENVELOPE, sa_budget, sa_kv_desc)
+                   SA_SCORE_ENVELOPE, sa_budget, sa_kv_desc, sa_paged_desc)
 
 lib = _abi.load()
 
@@ -352,3 +352,189 @@ def sparse_attn_get_device_status(ws: torch.Tensor, stream=None) -> int:
 
 def sparse_attn_status_string(code: int) -> str:
     return lib.sparse_attn_status_string(int(code)).decode()
+
+
+class PagedCache:
+    """A cache held in pages: k, v [n_pages, Hkv, page_size, 128], bf16 or
+    float8_e4m3fn, of the same strides (the last one 1), so token-major pages
+    ([n_pages, page_size, Hkv, 128].transpose(1, 2)) fit; page_table int32
+    [B, max_pages]; seq_len int32 [B], the tokens of each sequence with the
+    new ones of a call.  float8_e4m3fn: k_scale, v_scale uint8 [n_pages, Hkv,
+    page_size], a value being code * 2^(scale - 127).  Holds references to the
+    tensors so the pointers in `desc` stay valid."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor, *,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [n_pages, Hkv, page_size, D] tensors of one shape and type")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("k and v must be bf16 or float8_e4m3fn")
+        n_pages, Hkv, page_size, D = k.shape
+        if 0 in k.shape:
+            raise ValueError("k and v must not be empty")
+
+        def strides(t):  # the stride of an axis of one element says nothing: take one that fits
+            s = list(t.stride())
+            if D > 1 and s[3] != 1:
+                raise ValueError("k and v must have contiguous rows (last stride 1)")
+            if page_size == 1:
+                s[2] = D
+            if Hkv == 1:
+                s[1] = page_size * s[2]
+            if n_pages == 1:
+                s[0] = max(Hkv * s[1], page_size * s[2])
+            return s[:3]
+        page_stride, head_stride, token_stride = strides(k)
+        if strides(v) != strides(k):
+            raise ValueError("k and v must have the same strides")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+            raise ValueError("page_table must be contiguous int32 [B, max_pages]")
+        B, max_pages = page_table.shape
+        if seq_len.dtype != torch.int32 or tuple(seq_len.shape) != (B,) or not seq_len.is_contiguous():
+            raise ValueError("seq_len must be contiguous int32 [B]")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if e4m3 != (t is not None):
+                raise ValueError(f"{name} is needed with a float8_e4m3fn cache, and only with it")
+            if e4m3 and (t.dtype != torch.uint8 or tuple(t.shape) != (n_pages, Hkv, page_size)
+                         or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous uint8 [n_pages, Hkv, page_size]")
+        self.device = k.device
+        for t in (v, page_table, seq_len, k_scale, v_scale):
+            if t is not None and t.device != self.device:
+                raise ValueError("the tensors of a cache must be on one device")
+        self.k, self.v, self.page_table, self.seq_len = k, v, page_table, seq_len
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.n_kv_heads, self.page_size, self.batch = Hkv, page_size, B
+        self.desc = sa_paged_desc(B, Hkv, D, page_size, n_pages, _abi.SA_KV_E4M3 if e4m3 else _abi.SA_KV_BF16,
+                                  max_pages, k.data_ptr(), v.data_ptr(), page_stride, head_stride, token_stride,
+                                  _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), seq_len.data_ptr())
+
+
+def _on(kv: PagedCache, stream, tensors) -> int:
+    """The stream of a call on the cache's device: the given one, or that
+    device's current one.  All tensors of a call are on that device."""
+    dev = kv.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("the tensors of a call must be on the cache's device")
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _stream(stream)
+
+
+def _paged_call(kv: PagedCache, fn, where: str, *args) -> None:
+    """Run a call with the cache's device current."""
+    if kv.device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(kv.device):
+            st = fn(*args)
+    if st != 0:
+        raise SparseAttnError(st, where)
+
+
+def _rows(t: torch.Tensor, name: str, heads: int | None = None) -> int:
+    """The row stride (elements) of a packed bf16 [rows, heads, 128] array
+    whose heads lie one after another, so parts of a projection's rows fit."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be a bf16 [rows, heads, 128] tensor of the call's heads")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != 128 and t.shape[1] > 1):
+        raise ValueError(f"{name} must have its heads one after another in a row")
+    return s0 if t.shape[0] > 1 else t.shape[1] * 128
+
+
+def _row_off(row_off: torch.Tensor, kv: PagedCache) -> None:
+    if row_off.dtype != torch.int32 or row_off.dim() != 1 or row_off.shape[0] != kv.batch + 1 \
+            or not row_off.is_contiguous():
+        raise ValueError("row_off must be contiguous int32 [B + 1]")
+
+
+def _ws(ws: torch.Tensor | None) -> tuple[int | None, int]:
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def sparse_attn_paged_workspace_size(kv: PagedCache, n_q_heads: int) -> int:
+    return int(lib.sparse_attn_paged_workspace_size(C.byref(kv.desc), int(n_q_heads)))
+
+
+def make_paged_workspace(kv: PagedCache, n_q_heads: int, stream=None) -> torch.Tensor:
+    """Workspace of the paged-cache calls; calls that may overlap on the GPU
+    (other streams, other captured graphs) need one each."""
+    n = sparse_attn_paged_workspace_size(kv, n_q_heads)
+    if n == 0:
+        raise SparseAttnError(_abi.SA_ERR_INVALID, "sparse_attn_paged_workspace_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=kv.device)
+    _paged_call(kv, lib.sparse_attn_workspace_init, "sparse_attn_workspace_init", ws.data_ptr(), n,
+                _on(kv, stream, ()))
+    return ws
+
+
+def sparse_attn_cache_write(kv: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, row_off: torch.Tensor,
+                            ws: torch.Tensor | None = None, stream=None) -> None:
+    """Store the new rows (bf16 [rows, Hkv, 128], rows row_off[b] ..
+    row_off[b + 1] - 1 being the last tokens of sequence b) in the cache,
+    quantised if it holds e4m3.  ws: takes the status word; may be None."""
+    Hkv = kv.n_kv_heads
+    stride = _rows(k_new, "k_new", Hkv)
+    if v_new.shape[0] != k_new.shape[0] or _rows(v_new, "v_new", Hkv) != stride:
+        raise ValueError("k_new and v_new must have the same rows and strides")
+    _row_off(row_off, kv)
+    s = _on(kv, stream, (k_new, v_new, row_off, ws))
+    if k_new.shape[0] == 0:
+        return
+    _paged_call(kv, lib.sparse_attn_cache_write, "sparse_attn_cache_write", C.byref(kv.desc), k_new.data_ptr(),
+                v_new.data_ptr(), stride, row_off.data_ptr(), k_new.shape[0], *_ws(ws), s)
+
+
+def sparse_attn_cache_read(kv: PagedCache, first_token: int, k_out: torch.Tensor, v_out: torch.Tensor,
+                           ws: torch.Tensor | None = None, stream=None) -> None:
+    """Read tokens back into a contiguous bf16 cache [B, Hkv, cap, 128] (the k
+    and v of a KvCache): tokens first_token .. seq_len - 1 of every sequence,
+    or its last -first_token ones.  Other rows are left as they are."""
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous() or t.shape != k_out.shape \
+                or t.shape[0] != kv.batch or t.shape[1] != kv.n_kv_heads or t.shape[3] != 128:
+            raise ValueError(f"{name} must be a contiguous bf16 [B, Hkv, cap, 128] tensor")
+    s = _on(kv, stream, (k_out, v_out, ws))
+    _paged_call(kv, lib.sparse_attn_cache_read, "sparse_attn_cache_read", C.byref(kv.desc), int(first_token),
+                k_out.data_ptr(), v_out.data_ptr(), k_out.shape[2], *_ws(ws), s)
+
+
+def _attn_out(q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None) -> int:
+    if out.shape != q.shape or not out.is_contiguous() or out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out must be contiguous fp32 or bf16 [rows, Hq, 128]")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != q.shape[:2]):
+        raise ValueError("lse must be contiguous fp32 [rows, Hq]")
+    return _abi.SA_OUT_BF16 if out.dtype == torch.bfloat16 else _abi.SA_OUT_F32
+
+
+def sparse_attn_chunk(kv: PagedCache, q: torch.Tensor, row_off: torch.Tensor, scale: float, window: int, sinks: int,
+                      out: torch.Tensor, lse: torch.Tensor | None, ws: torch.Tensor, stream=None) -> None:
+    """Causal attention of the new rows q (bf16 [rows, Hq, 128]; rows
+    row_off[b] .. row_off[b + 1] - 1 are the last tokens of sequence b, whose
+    keys and values the cache already holds) over the cache.  window > 0: a row
+    sees its last `window` tokens, itself included, and the first `sinks`."""
+    stride = _rows(q, "q")
+    out_dtype = _attn_out(q, out, lse)
+    _row_off(row_off, kv)
+    s = _on(kv, stream, (q, row_off, out, lse, ws))
+    if q.shape[0] == 0:
+        return
+    _paged_call(kv, lib.sparse_attn_chunk, "sparse_attn_chunk", C.byref(kv.desc), q.data_ptr(), stride, q.shape[1],
+                row_off.data_ptr(), q.shape[0], int(window), int(sinks), float(scale), out.data_ptr(), out_dtype,
+                _ptr(lse), *_ws(ws), s)
+
+
+def sparse_attn_paged_decode(kv: PagedCache, q: torch.Tensor, scale: float, window: int, sinks: int,
+                             out: torch.Tensor, lse: torch.Tensor | None, ws: torch.Tensor, stream=None) -> None:
+    """One row per sequence: q bf16 [B, Hq, 128], row b the newest token of
+    sequence b; otherwise as sparse_attn_chunk."""
+    stride = _rows(q, "q")
+    if q.shape[0] != kv.batch:
+        raise ValueError("q must have one row per sequence")
+    out_dtype = _attn_out(q, out, lse)
+    s = _on(kv, stream, (q, out, lse, ws))
+    _paged_call(kv, lib.sparse_attn_paged_decode, "sparse_attn_paged_decode", C.byref(kv.desc), q.data_ptr(), stride,
+                q.shape[1], int(window), int(sinks), float(scale), out.data_ptr(), out_dtype, _ptr(lse), *_ws(ws), s)

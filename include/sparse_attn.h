@@ -392,6 +392,112 @@ sa_status sparse_attn_decode_static(const sa_kv_desc* kv, const void* q, int32_t
                                     int32_t max_sel, float* out, float* lse,
                                     int32_t* device_status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * (g) The paged cache: keys and values in pages that a page table maps, in
+ * bf16 or quantised to e4m3, with dense and windowed attention over it.  The
+ * pages describe no such call; these serve what the calls above leave to the
+ * caller: a cache that grows page by page, shares memory between sequences
+ * and holds 8 bits per value, filled by whole chunks of new tokens, attended
+ * densely by chunks and by single tokens, and read back into the contiguous
+ * bf16 view (sa_kv_desc) that selection and router take.
+ *
+ * Token t of sequence b lies in pool page page_table[b][t / page_size], slot
+ * t % page_size.  seq_len[b] = N_b >= 0 counts the tokens of the sequence,
+ * the new ones of the call included: the m_b new rows of a call are tokens
+ * N_b - m_b .. N_b - 1.  Rows are given packed: row_off [B + 1] (device,
+ * ascending) says that rows row_off[b] .. row_off[b + 1] - 1 of the row
+ * arrays are the new rows of sequence b; rows outside every such range are
+ * neither read nor written.
+ *
+ * SA_KV_E4M3: a value is code * 2^(E - 127), E the scale byte of its (page,
+ * head, slot) row.  A row of values x is held with the smallest power of two
+ * that leaves it within e4m3's 448: k = min { k : max |x| <= 448 * 2^k },
+ * clipped to [-124, 119]; E = k + 127; code = x * 2^-k (exact) rounded to
+ * nearest even, saturating.  code * 2^k is exactly a bf16, so a quantised
+ * cache is a bf16 cache of the rounded values in every call here.
+ *
+ * Checks found on the device set SA_ERR_DEVICE_CHECK in the status word of
+ * ws: a sequence with N_b outside [0, max_pages * page_size] or with a row
+ * range outside [0, n_rows] counts as having no tokens or no rows; rows
+ * before the sequence's first token (m_b > N_b) are not stored and see
+ * nothing (an empty slot of a decode batch, N_b = 0, is no error: its row of
+ * sparse_attn_paged_decode sees nothing); a token whose page is outside [0, n_pages) is not stored, not read
+ * and not attended.  Pages that no token of the call needs are not looked at
+ * (entries of pages that a window has passed may hold anything). */
+typedef enum {
+  SA_KV_BF16 = 0,
+  SA_KV_E4M3 = 1
+} sa_kv_dtype;
+
+typedef struct {
+  int32_t batch;              /* B >= 1 */
+  int32_t n_kv_heads;         /* Hkv >= 1 */
+  int32_t head_dim;           /* must be 128 */
+  int32_t page_size;          /* tokens of a page: multiple of 16 in [16, 256] */
+  int64_t n_pages;            /* pages of the pool, 1 .. 2^31 - 1 */
+  int32_t dtype;              /* sa_kv_dtype of k and v */
+  int32_t max_pages;          /* page table entries of a sequence; max_pages * page_size < 2^31 */
+  void* k;                    /* value d of (page, head, slot) at k + page * page_stride + head * */
+  void* v;                    /*   head_stride + slot * token_stride + d; 16-byte aligned */
+  int64_t page_stride;        /* elements, positive multiples of 16 bytes; so head-major and */
+  int64_t head_stride;        /*   token-major pages and parts of larger arrays all fit */
+  int64_t token_stride;       /* >= 128 */
+  uint8_t* k_scale;           /* SA_KV_E4M3: [n_pages][n_kv_heads][page_size], 16-byte aligned; else null */
+  uint8_t* v_scale;
+  const int32_t* page_table;  /* [B][max_pages] */
+  const int32_t* seq_len;     /* [B] */
+} sa_paged_desc;
+
+/* Bytes of the workspace of sparse_attn_chunk and sparse_attn_paged_decode
+ * (0 on invalid arguments): a status word and scratch for split partial
+ * results.  256-byte aligned, zeroed once by sparse_attn_workspace_init.
+ * Calls that may overlap on the GPU need separate workspaces.
+ * sparse_attn_cache_write and _read use its status word only. */
+size_t sparse_attn_paged_workspace_size(const sa_paged_desc* kv, int32_t n_q_heads);
+
+/* (g1) Store the new rows in the cache, quantising them if it holds e4m3.
+ * k_new, v_new: bf16, value d of (row, head) at row * row_stride + head * 128
+ * + d (elements; row_stride a multiple of 8, >= n_kv_heads * 128: parts of a
+ * projection's rows fit), 16-byte aligned.  No two tokens of a call may share
+ * a (page, slot).  n_rows: rows of the arrays; 0 stores nothing. */
+sa_status sparse_attn_cache_write(const sa_paged_desc* kv, const void* k_new, const void* v_new,
+                                  int64_t row_stride, const int32_t* row_off, int32_t n_rows,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* (g2) Read tokens [t0_b, N_b) back: k_out, v_out bf16 [B][n_kv_heads]
+ * [cap_tokens][128], the contiguous cache of sa_kv_desc; row t holds token t.
+ * first_token as in sparse_attn_build_meta (>= 0: t0_b = first_token; < 0:
+ * t0_b = max(0, N_b + first_token)).  Rows outside the range are not written;
+ * tokens at and past cap_tokens are not read back (SA_ERR_DEVICE_CHECK). */
+sa_status sparse_attn_cache_read(const sa_paged_desc* kv, int32_t first_token, void* k_out,
+                                 void* v_out, int64_t cap_tokens, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* (g3) Attention of a chunk of new rows of every sequence over its cache,
+ * which already holds the rows' own keys and values.  Row i of sequence b is
+ * at position p = N_b - m_b + i and sees token t <= p if
+ *   window == 0, or t > p - window (the window, its own token included), or
+ *   t < sinks (the first tokens, which stay visible).
+ * q: bf16, value d of (row, query head) at row * q_row_stride + head * 128 +
+ * d (q_row_stride a multiple of 8, >= n_q_heads * 128), 16-byte aligned.
+ * z = scale * q . k, softmax in fp32; out [n_rows][n_q_heads][128], fp32 or
+ * bf16 (16-byte aligned); lse (nullable) fp32 [n_rows][n_q_heads], the natural
+ * logarithm of the sum of exp(z).  A row that sees nothing gets out = 0 and
+ * lse = -inf.  What is held past N_b, or where no row of the sequence looks,
+ * may be anything, NaN included.  Any m_b from 0 on; lengths are read on the
+ * device only, so a captured call replays with other lengths.  Two launches. */
+sa_status sparse_attn_chunk(const sa_paged_desc* kv, const void* q, int64_t q_row_stride,
+                            int32_t n_q_heads, const int32_t* row_off, int32_t n_rows,
+                            int32_t window, int32_t sinks, float scale, void* out,
+                            int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* (g4) The single-token form: one row per sequence (row b at position
+ * N_b - 1), otherwise as sparse_attn_chunk. */
+sa_status sparse_attn_paged_decode(const sa_paged_desc* kv, const void* q, int64_t q_row_stride,
+                                   int32_t n_q_heads, int32_t window, int32_t sinks, float scale,
+                                   void* out, int32_t out_dtype, float* lse, void* ws,
+                                   size_t ws_bytes, void* stream);
+
 /* Static description of a status code (never null). */
 const char* sparse_attn_status_string(sa_status s);
 
