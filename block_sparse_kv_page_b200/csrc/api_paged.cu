@@ -4,15 +4,59 @@
 // Workspace: the layout of the other calls (api.cu): the status word at 0, the
 // unit counters (not used here, left as they are), per-call scratch from
 // kScratch on.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
 
 namespace sa {
+
+cudaError_t allow_smem(const void* func, size_t bytes) {
+  struct Entry {
+    std::atomic<const void*> func{nullptr};
+    std::atomic<uint64_t> devices{0};  // bit d: set on device d
+  };
+  static Entry table[16];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  Entry* mine = nullptr;
+  for (Entry& t : table) {
+    const void* f = t.func.load(std::memory_order_acquire);
+    if (f == nullptr && t.func.compare_exchange_strong(f, func)) f = func;
+    if (f == func) {
+      mine = &t;
+      break;
+    }
+  }
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (mine && (mine->devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && mine) mine->devices.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Scratch of the attention calls, from kScratch on.
+struct PagedScratch {
+  size_t parts, xbuf, recs, total;
+};
+PagedScratch paged_scratch() {
+  const size_t sms = (size_t)device_sm_count();
+  PagedScratch s;
+  s.parts = kScratch;
+  s.xbuf = s.parts + align256(sms * 2 * 2 * 128 * kChunkPart * sizeof(float));
+  s.recs = s.xbuf + align256(sms * 128 * kChunkPart * sizeof(float));
+  s.total = s.recs + align256(sms * sizeof(ChunkRec));
+  return s;
+}
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -88,6 +132,35 @@ sa_status check_heads(const sa_paged_desc* kv, int n_q_heads, int* G) {
   return SA_OK;
 }
 
+sa_status chunk(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
+  ChunkArgs a{};
+  const PagedView& kv = p.kv;
+  const int blk = chunk_block_tokens(p.out != nullptr);
+  a.p = p;
+  a.scale_log2 = p.scale * kLog2e;
+  a.R = 128 / p.G;
+  a.hb = std::gcd(kv.page_size, blk);
+  const unsigned long long qd[3] = {kHeadDim, (unsigned long long)p.Hq, (unsigned long long)p.n_rows};
+  const unsigned long long qs[2] = {kHeadDim * 2, (unsigned long long)p.q_row_stride * 2};
+  const unsigned qb[3] = {64, (unsigned)p.G, (unsigned)a.R};
+  if (!encode_tmap_nd(&a.tmap_q, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, qd, qs, qb, true)) return SA_ERR_CUDA;
+  if (!kv.e4m3) {
+    const unsigned long long d[4] = {kHeadDim, (unsigned long long)kv.page_size, (unsigned long long)kv.Hkv,
+                                     (unsigned long long)kv.n_pages};
+    const unsigned long long s[3] = {(unsigned long long)kv.token_stride, (unsigned long long)kv.head_stride,
+                                     (unsigned long long)kv.page_stride};
+    const unsigned b[4] = {64, (unsigned)a.hb, 1, 1};
+    if (!encode_tmap_nd(&a.tmap_k, kv.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, d, s, b, true) ||
+        !encode_tmap_nd(&a.tmap_v, kv.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, d, s, b, true))
+      return SA_ERR_CUDA;
+  }
+  const PagedScratch sc = paged_scratch();
+  a.parts = (float*)(ws + sc.parts);
+  a.xbuf = (float*)(ws + sc.xbuf);
+  a.recs = (ChunkRec*)(ws + sc.recs);
+  return launched(launch_chunk(a, device_sm_count(), st));
+}
+
 sa_status paged_attention(const sa_paged_desc* kv, const void* q, int64_t q_row_stride, int n_q_heads,
                           const int32_t* row_off, int n_rows, int window, int sinks, float scale, void* out,
                           int out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream) {
@@ -116,7 +189,10 @@ sa_status paged_attention(const sa_paged_desc* kv, const void* q, int64_t q_row_
   else a.out = (float*)out;
   a.lse = lse;
   a.status = (int*)ws;
-  return launched(launch_paged_attn(a, (cudaStream_t)stream));
+  // a window that no position passes is none (and keeps p - window in range)
+  if ((long long)window > (long long)kv->max_pages * kv->page_size) a.window = 0;
+  if (!row_off) return launched(launch_paged_attn(a, (cudaStream_t)stream));
+  return chunk(a, (unsigned char*)ws, (cudaStream_t)stream);
 }
 
 }  // namespace
@@ -129,7 +205,7 @@ extern "C" {
 size_t sparse_attn_paged_workspace_size(const sa_paged_desc* kv, int32_t n_q_heads) {
   int G;
   if (check_paged(kv) != SA_OK || check_heads(kv, n_q_heads, &G) != SA_OK) return 0;
-  return kScratch;
+  return paged_scratch().total;
 }
 
 sa_status sparse_attn_cache_write(const sa_paged_desc* kv, const void* k_new, const void* v_new,

@@ -1,0 +1,920 @@
+// Attention of a chunk of new rows of every sequence over its paged cache, on
+// tcgen05.
+//
+// Mathematics: row i of sequence b at position p = N_b - m_b + i, query head h
+// of KV head g: z_t = scale q . k_t over the visible tokens t (t <= p, inside
+// the window or among the first tokens), out = sum exp(z_t - lse) v_t, by one
+// pass over the tokens with a running reference maximum and sum.
+//
+// Units.  A query vector is a (row, query head) pair.  The G heads of a KV head
+// and R = floor(128 / G) consecutive rows make a tile of up to 128 vectors (M of
+// the MMA); two tiles (2 R rows) make a pair that shares every K/V block of BLK
+// tokens.  Where a pair has rows for one tile only, both tile slots take that
+// tile and every other block each, and merge at the end.
+//
+// Split.  The work is the list of (sequence, KV head, pair) with nb blocks
+// each; the grid is one CTA per SM and takes equal runs of nb + kC0 over that
+// list, cut anywhere, so that neither the number of pairs nor the causal
+// triangle leaves SMs idle and a few rows over a long cache spread over every
+// SM.  Every CTA computes the list's prefix from the lengths on the device
+// (no host copy: a captured launch replays with other lengths).  A pair cut
+// between CTAs leaves unnormalised partial results in the workspace, which
+// combine_kernel merges in CTA order: results do not depend on scheduling.
+//
+// CTA, warp-specialised, every wait bounded:
+//   warps 0-3 / 4-7  softmax of tile slot 0 / 1: thread = query vector (TMEM
+//                    lane), its whole row of BLK scores in registers;
+//   warp 8           TMA of the queries and, for a bf16 cache, of the K and V
+//                    tiles (boxes of up to BLK rows inside a page; boxes that
+//                    no row of the pair needs, or whose page is bad, are
+//                    fetched from past the pool's end and so read as zeros);
+//   warps 9, 10      MMA issue of slot 0 / 1 (one thread each): S = Q K^T into
+//                    the slot's S columns, then, once the softmax has written
+//                    P over S, O += P V;
+//   warps 12-15      (e4m3 cache) turn the codes of K and V into bf16 tiles:
+//                    code * 2^k is exactly a bf16, so the products are those of
+//                    a bf16 cache of the rounded values.
+// Roles run ahead of each other over block and segment boundaries; only the
+// mbarriers order them.
+//
+// P is rounded to bf16 where the output is bf16 (its error, 2^-9 per weight, is
+// that of the output's own rounding); for fp32 outputs it is split into three
+// bf16 terms (24 bits) on blocks of 64 tokens.
+#include "paged.cuh"
+#include "tcgen05.cuh"
+#include "internal.h"
+
+namespace sa {
+namespace {
+
+constexpr int kC0 = 2;              // cost of starting a pair, in blocks
+constexpr int kMinShare = 4 + kC0;  // least work of a CTA
+constexpr int kInfo = 8;
+constexpr int kQTileBytes = 2 * 128 * 128;
+constexpr int kRingBytes = 128 * 1024;
+constexpr uint32_t kColS = 0, kColO = 256;  // slot t: S / P at 128 t, O at 256 + 128 t
+
+template <int TERMS>
+struct Shape {
+  static constexpr int BLK = TERMS == 1 ? 128 : 64;   // tokens of a block
+  static constexpr int kHalf = BLK * 128;             // 64 dims of a tile
+  static constexpr int kSlot = 2 * kHalf;             // a K or V tile
+  static constexpr int NS = kRingBytes / kSlot;       // ring slots (K, V alternating)
+  static constexpr int kOffRing = 2 * kQTileBytes;
+  static constexpr int kOffBars = kOffRing + kRingBytes;
+  static constexpr int kNumBars = 2 * NS + 2 + 6 + kInfo + 2 + 1;
+  static constexpr int kOffInfo = kOffBars + 8 * kNumBars;
+  static constexpr int kSmem = 1024 + kOffInfo + 4 * kInfo + 16;
+};
+
+template <int R>
+SA_DEV void reg_alloc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R));
+}
+template <int R>
+SA_DEV void reg_dealloc() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R));
+}
+
+SA_DEV float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// MN-major view of V: 8-token atoms 1 KiB apart, the two 64-dim halves apart
+// by HALF bytes.
+template <int HALF>
+SA_DEV uint64_t v_desc(const unsigned char* v) {
+  return (tc::smem_desc_sw128(v) & ~(0x3FFFull << 16)) | ((uint64_t)(HALF >> 4) << 16);
+}
+
+// Blocks of pair j of a sequence: tokens [0, S) (first tokens) and [lo, p1].
+struct Geom {
+  int rows, p0, p1, lo, S, sb, wb0, nb;
+};
+template <int BLK>
+SA_DEV Geom pair_geom(const ChunkArgs& a, int N, int m, int j) {
+  Geom q;
+  q.rows = min(2 * a.R, m - 2 * a.R * j);
+  q.p0 = N - m + 2 * a.R * j;
+  q.p1 = q.p0 + q.rows - 1;
+  q.lo = a.p.window && q.p0 >= a.p.window ? q.p0 - a.p.window + 1 : 0;
+  q.S = a.p.window ? min(a.p.sinks, q.p1 + 1) : 0;
+  if (q.p1 < 0) {
+    q.sb = q.wb0 = q.nb = 0;
+    return q;
+  }
+  q.wb0 = q.lo / BLK;
+  q.sb = min((q.S + BLK - 1) / BLK, q.wb0);
+  q.nb = q.sb + q.p1 / BLK - q.wb0 + 1;
+  return q;
+}
+
+// A run [i0, i1) of the blocks of one pair, on this CTA.
+struct Seg : Geom {
+  int b, g, N, row0;          // row0: first row of the pair in the row arrays
+  int i0, i1, cost;
+  bool single;                // rows for one tile only
+  unsigned long long w;       // where the pair's work begins
+};
+
+struct Plan {
+  int b, g, j, off, n_cta;
+  unsigned long long w0, w1, total;
+};
+
+// Walks the segments of a CTA; every role has its own.
+template <int BLK>
+struct Cursor {
+  int b, g, j, off, N, m, r0, pairs;
+  unsigned long long w, rem;
+  SA_DEV Cursor(const ChunkArgs& a, const Plan& p)
+      : b(p.b), g(p.g), j(p.j), off(p.off), N(0), m(0), r0(0), pairs(0), w(p.w0 - p.off), rem(p.w1 - p.w0) {
+    if (rem) load(a);
+  }
+  SA_DEV void load(const ChunkArgs& a) {
+    for (; b < a.p.kv.B; ++b) {
+      m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, a.p.status);
+      if (m > 0) break;
+    }
+    if (b < a.p.kv.B) {
+      N = paged_tokens(a.p.kv, b, a.p.status);
+      pairs = (m + 2 * a.R - 1) / (2 * a.R);
+    }
+  }
+  SA_DEV bool next(const ChunkArgs& a, Seg& s) {
+    while (rem && b < a.p.kv.B) {
+      static_cast<Geom&>(s) = pair_geom<BLK>(a, N, m, j);
+      s.cost = s.nb + kC0;
+      const int take = (int)min(rem, (unsigned long long)(s.cost - off));
+      const int from = off, to = off + take;
+      rem -= take;
+      s.b = b;
+      s.g = g;
+      s.N = N;
+      s.row0 = r0 + 2 * a.R * j;
+      s.i0 = min(max(from - kC0, 0), s.nb);
+      s.i1 = min(max(to - kC0, 0), s.nb);
+      s.single = s.rows <= a.R;
+      s.w = w;
+      if (to == s.cost) {
+        w += s.cost;
+        off = 0;
+        if (++j == pairs) {
+          j = 0;
+          if (++g == a.p.kv.Hkv) {
+            g = 0;
+            ++b;
+            load(a);
+          }
+        }
+      }
+      if (s.i1 > s.i0 || (s.nb == 0 && from == 0)) return true;
+    }
+    return false;
+  }
+};
+
+// Work of the sequences b (one per thread of a converged warp), one KV head.
+template <int BLK>
+SA_DEV unsigned long long seq_work(const ChunkArgs& a, int b) {
+  int N = 0, m = 0, r0;
+  if (b < a.p.kv.B) {
+    m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, a.p.status);
+    N = paged_tokens(a.p.kv, b, a.p.status);
+  }
+  const int pairs = (m + 2 * a.R - 1) / (2 * a.R);
+  unsigned long long w = 0;
+  if (pairs <= 8)
+    for (int j = 0; j < pairs; ++j) w += pair_geom<BLK>(a, N, m, j).nb + kC0;
+  unsigned many = __ballot_sync(0xffffffffu, pairs > 8);  // long ones: the whole warp
+  const int lane = threadIdx.x & 31;
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    const int sn = __shfl_sync(0xffffffffu, N, src), sm = __shfl_sync(0xffffffffu, m, src);
+    const int sp = __shfl_sync(0xffffffffu, pairs, src);
+    unsigned long long x = 0;
+    for (int j = lane; j < sp; j += 32) x += pair_geom<BLK>(a, sn, sm, j).nb + kC0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == src) w = x;
+  }
+  return w;
+}
+
+// Exclusive prefix over the block and its total (every thread calls it).
+SA_DEV unsigned long long scan64(unsigned long long v, unsigned long long* scratch, unsigned long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  unsigned long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  unsigned long long base = 0, tot = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) base += scratch[w];
+    tot += scratch[w];
+  }
+  __syncthreads();
+  total = tot;
+  return base + x - v;
+}
+
+// This CTA's share of the work (every thread calls it; scratch: 18 words).
+template <int BLK>
+SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratch) {
+  const int T = blockDim.x, tid = threadIdx.x, B = a.p.kv.B;
+  const unsigned long long H = a.p.kv.Hkv;
+  unsigned long long total = 0, w = 0, t, ex = 0;
+  for (int base = 0; base < B; base += T) {
+    w = seq_work<BLK>(a, base + tid) * H;
+    ex = scan64(w, scratch, t) + total;
+    total += t;
+  }
+  const unsigned long long most = total / kMinShare;
+  const unsigned long long n = most < 1 ? 1 : (most < gridDim.x ? most : gridDim.x);
+  const unsigned long long c = blockIdx.x;
+  if (tid == 0) {
+    plan->total = total;
+    plan->n_cta = (int)n;
+    plan->w0 = c < n ? total * c / n : 0;
+    plan->w1 = c < n ? total * (c + 1) / n : 0;
+    plan->b = B;
+    plan->g = plan->j = plan->off = 0;
+  }
+  __syncthreads();
+  const unsigned long long w0 = plan->w0;
+  if (plan->w1 == w0) return;
+  unsigned long long run = 0;
+  for (int base = 0; base < B; base += T) {
+    if (B > T) {
+      w = seq_work<BLK>(a, base + tid) * H;
+      ex = scan64(w, scratch, t) + run;
+      run += t;
+    }
+    if (w && ex <= w0 && w0 < ex + w) {
+      plan->b = base + tid;
+      scratch[16] = w0 - ex;
+      scratch[17] = w / H;
+    }
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const unsigned long long in = scratch[16], per = scratch[17];
+    const int b = plan->b, g = (int)(in / per);
+    const unsigned long long off = in - (unsigned long long)g * per;
+    int r0;
+    const int m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, nullptr), N = paged_tokens(a.p.kv, b, nullptr);
+    const int pairs = (m + 2 * a.R - 1) / (2 * a.R);
+    unsigned long long before = 0;
+    for (int j0 = 0; j0 < pairs; j0 += 32) {
+      const int j = j0 + tid;
+      const unsigned long long cst = j < pairs ? pair_geom<BLK>(a, N, m, j).nb + kC0 : 0;
+      unsigned long long x = cst;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (tid >= o) x += y;
+      }
+      x += before;
+      if (cst && x - cst <= off && off < x) {
+        plan->g = g;
+        plan->j = j;
+        plan->off = (int)(off - (x - cst));
+      }
+      before = __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// 4 codes -> two bf16 pairs: a code's 7 low bits are the exponent and mantissa
+// of a bf16 2^120 times smaller, subnormals included; m2 holds 2^(120 + k) (and
+// then `more`, another power of two, for rows past 2^127) in both halves.
+SA_DEV uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+SA_DEV uint2 bf16_of_codes(uint32_t w, uint32_t m2) {
+  const uint32_t odd = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), m2);
+  const uint32_t even = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), m2);
+  return make_uint2(prmt(even, odd, 0x5410), prmt(even, odd, 0x7632));
+}
+
+template <bool E4M3, int TERMS>
+__global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+  using Sh = Shape<TERMS>;
+  constexpr int BLK = Sh::BLK, NS = Sh::NS;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ Plan s_plan;
+  __shared__ unsigned long long s_scan[18];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* qs = base;
+  unsigned char* ring = base + Sh::kOffRing;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(base + Sh::kOffBars);
+  uint64_t* kv_empty = kv_full + NS;
+  uint64_t* q_full = kv_empty + NS;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;   // [slot]
+  uint64_t* p_full = s_full + 2;    // [slot]
+  uint64_t* o_full = p_full + 2;    // [slot]
+  uint64_t* info_full = o_full + 2;
+  uint64_t* x_full = info_full + kInfo;
+  uint64_t* x_empty = x_full + 1;
+  uint64_t* drain = x_empty + 1;
+  volatile uint32_t* info = reinterpret_cast<uint32_t*>(base + Sh::kOffInfo);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float ninf = -__int_as_float(0x7f800000);
+  int* status = a.p.status;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(kv_full + s, E4M3 ? 4 : 1);
+      mbar_init(kv_empty + s, 2);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full + t, 1);
+      mbar_init(p_full + t, 4);
+      mbar_init(o_full + t, 1);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(info_full + i, 1);
+    mbar_init(x_full, 4);
+    mbar_init(x_empty, 4);
+    mbar_init(drain, 2);
+    fence_barrier_init();
+    prefetch_tmap(&a.tmap_q);
+    if (!E4M3) {
+      prefetch_tmap(&a.tmap_k);
+      prefetch_tmap(&a.tmap_v);
+    }
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(&s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  grid_dep_wait();
+  make_plan<BLK>(a, &s_plan, s_scan);
+  if (tid == 0) a.recs[blockIdx.x] = ChunkRec{0, 0, 0, 0, 0};
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  const PagedView& kv = a.p.kv;
+  Cursor<BLK> cur(a, s_plan);
+  Seg sg;
+
+  if (warp >= 8 && warp < 12) {
+    if (E4M3) reg_dealloc<56>();
+    else reg_dealloc<72>();
+    if (warp == 8) {
+      // ---- producer
+      int n = 0, segs = 0;
+      bool ok = true;
+      const int hb = a.hb, nbox = BLK / hb;
+      while (ok && cur.next(a, sg)) {
+        if (sg.i0 == sg.i1) continue;
+        if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1u, status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const int tiles = sg.single ? 1 : 2;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * 2 * 128 * a.p.G * a.R));
+        __syncwarp();
+        if (lane < 2 * tiles)
+          tma_load_3d(qs + (lane >> 1) * kQTileBytes + (lane & 1) * (128 * 128), &a.tmap_q, 64 * (lane & 1),
+                      sg.g * a.p.G, sg.row0 + (lane >> 1) * a.R, q_full);
+        ++segs;
+        for (int i = sg.i0; i < sg.i1; ++i, ++n) {
+          const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
+          // this lane's box: rows sub * hb .. of half (lane & 1)
+          const int sub = lane >> 1;
+          int page = -1, slot = 0;
+          uint32_t bad = 0;
+          if (sub < nbox) {
+            const int t0 = kb0 + sub * hb;
+            const bool need = t0 < sg.S || (t0 <= sg.p1 && t0 + hb > sg.lo);
+            if (need) {
+              const int p = t0 / kv.page_size;
+              slot = t0 - p * kv.page_size;
+              page = paged_page(kv, sg.b, p, status);
+              if (page < 0) bad = ((1u << (hb / 16)) - 1u) << (sub * (hb / 16));
+            }
+          }
+          bad = __reduce_or_sync(0xffffffffu, bad);
+          const int ks = (2 * n) % NS, vs = ks + 1;
+          const uint32_t use = (uint32_t)((2 * n) / NS);
+          if (use > 0) ok = mbar_wait(kv_empty + ks, (use - 1) & 1u, status);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            info[n % kInfo] = bad;
+            mbar_arrive(info_full + n % kInfo);
+          }
+          if (!E4M3) {
+            const int at = page < 0 ? (int)kv.n_pages : page;  // past the pool: zeros
+            if (lane == 0) mbar_arrive_expect_tx(kv_full + ks, Sh::kSlot);
+            __syncwarp();
+            if (sub < nbox)
+              tma_load_4d(ring + ks * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128, &a.tmap_k, 64 * (lane & 1),
+                          slot, sg.g, at, kv_full + ks);
+            if (use > 0) ok = mbar_wait(kv_empty + vs, (use - 1) & 1u, status);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              ++n;  // the K tile was issued
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(kv_full + vs, Sh::kSlot);
+            __syncwarp();
+            if (sub < nbox)
+              tma_load_4d(ring + vs * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128, &a.tmap_v, 64 * (lane & 1),
+                          slot, sg.g, at, kv_full + vs);
+          }
+        }
+      }
+      // every copy issued has landed before the CTA ends (bounded)
+      if (segs > 0) mbar_wait(q_full, (segs - 1) & 1u, nullptr);
+      if (!E4M3) {
+        for (int x = max(0, n - NS / 2); x < n; ++x) {
+          mbar_wait(kv_full + (2 * x) % NS, ((2 * x) / NS) & 1u, nullptr);
+          if (ok) mbar_wait(kv_full + (2 * x) % NS + 1, ((2 * x) / NS) & 1u, nullptr);
+        }
+      }
+    } else if (warp < 11 && lane == 0) {
+      // ---- MMA issue of slot t
+      const int t = warp - 9;
+      const uint32_t idesc_s = tc::idesc_f32acc(tc::kFmtBF16, 128, BLK);
+      const uint32_t idesc_o = tc::idesc_f32acc(tc::kFmtBF16, 128, kHeadDim) | (1u << 16);  // V MN-major
+      const uint32_t ts = tmem + kColS + 128u * t, to = tmem + kColO + 128u * t;
+      int n = 0, segs = 0;
+      uint32_t cnt = 0;
+      bool ok = true;
+      while (ok && cur.next(a, sg)) {
+        if (sg.i0 == sg.i1) continue;
+        const int n_end = n + sg.i1 - sg.i0;
+        const int step = sg.single ? 2 : 1;
+        int last = sg.single ? n_end - 1 - (((n_end - 1) & 1) ^ t) : n_end - 1;  // this slot's last block
+        if (last < n) last = -1;
+        if (!(ok = mbar_wait(q_full, segs & 1u, status))) break;
+        tc::fence_after_sync();
+        ++segs;
+        if (last < 0) mbar_arrive(q_empty);
+        const unsigned char* qt = qs + (sg.single ? 0 : t * kQTileBytes);
+        bool first = true;
+        for (; n < n_end; ++n) {
+          const int ks = (2 * n) % NS, vs = ks + 1;
+          const uint32_t ph = (uint32_t)((2 * n) / NS) & 1u;
+          if (!(ok = mbar_wait(kv_full + ks, ph, status))) break;
+          if (step == 2 && (n & 1) != t) {  // the other slot's block
+            mbar_arrive(kv_empty + ks);
+            if (!(ok = mbar_wait(kv_full + vs, ph, status))) break;
+            mbar_arrive(kv_empty + vs);
+            continue;
+          }
+          tc::fence_after_sync();
+          const unsigned char* kt = ring + ks * Sh::kSlot;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16_ss(ts, tc::smem_desc_sw128(qt + c * (128 * 128) + 32 * k),
+                              tc::smem_desc_sw128(kt + c * Sh::kHalf + 32 * k), idesc_s, (c | k) != 0);
+          tc::commit(s_full + t);
+          tc::commit(kv_empty + ks);
+          if (n == last) tc::commit(q_empty);
+          if (!(ok = mbar_wait(kv_full + vs, ph, status))) break;
+          if (!(ok = mbar_wait(p_full + t, cnt & 1u, status))) break;
+          tc::fence_after_sync();
+          ++cnt;
+          const unsigned char* vt = ring + vs * Sh::kSlot;
+#pragma unroll
+          for (int x = 0; x < TERMS; ++x)
+#pragma unroll
+            for (int j = 0; j < BLK / 16; ++j)
+              tc::mma_bf16_ts(to, ts + (uint32_t)(x * (BLK / 2) + 8 * j), v_desc<Sh::kHalf>(vt + 16 * 128 * j), idesc_o,
+                              !first || (x | j) != 0);
+          first = false;
+          tc::commit(kv_empty + vs);
+          if (n == last) tc::commit(o_full + t);
+        }
+        if (!ok) break;
+      }
+      // every MMA issued has completed before TMEM is freed (bounded)
+      tc::commit(drain);
+      mbar_wait(drain, 0, nullptr);
+    }
+  } else if (warp >= 12) {
+    // ---- e4m3 -> bf16: 8 threads per row, 16 rows at a time
+    if (E4M3) {
+      reg_dealloc<88>();
+      const int x = tid - 384, c = x & 7, r16 = x >> 3;
+      int n = 0;
+      bool ok = true;
+      while (ok && cur.next(a, sg)) {
+        for (int i = sg.i0; ok && i < sg.i1; ++i, ++n) {
+          const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
+          const int ks = (2 * n) % NS;
+          const uint32_t use = (uint32_t)((2 * n) / NS);
+          long long off[BLK / 16];
+          uint32_t sc[BLK / 16];  // K scale | V scale << 8
+#pragma unroll
+          for (int s = 0; s < BLK / 16; ++s) {
+            const int t = kb0 + 16 * s + r16;
+            off[s] = -1;
+            sc[s] = 0;
+            if (t < sg.S || (t >= sg.lo && t <= sg.p1)) {
+              const int p = t / kv.page_size, slot = t - p * kv.page_size;
+              const int page = paged_page(kv, sg.b, p, nullptr);
+              if (page >= 0) {
+                off[s] = paged_offset(kv, page, sg.g, slot) + 16 * c;
+                const size_t at = scale_index(kv, page, sg.g, slot);
+                sc[s] = (uint32_t)__ldg(kv.k_scale + at) | ((uint32_t)__ldg(kv.v_scale + at) << 8);
+              }
+            }
+          }
+#pragma unroll 1
+          for (int w = 0; w < 2 && ok; ++w) {
+            uint4 code[BLK / 16];
+#pragma unroll
+            for (int s = 0; s < BLK / 16; ++s)
+              code[s] = off[s] >= 0 ? ldg_nc128((w ? kv.v : kv.k) + off[s]) : make_uint4(0u, 0u, 0u, 0u);
+            if (use > 0) ok = mbar_wait(kv_empty + ks + w, (use - 1) & 1u, status);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            unsigned char* dst = ring + (ks + w) * Sh::kSlot + (c >> 2) * Sh::kHalf;
+#pragma unroll
+            for (int s = 0; s < BLK / 16; ++s) {
+              const int k = (int)((sc[s] >> (8 * w)) & 255u) - 127;  // the row's scale is 2^k
+              const uint32_t m1 = (uint32_t)(min(max(120 + k, -126), 127) + 127) << 7;
+              const uint32_t m2 = m1 | (m1 << 16);
+              uint2 o[4] = {bf16_of_codes(code[s].x, m2), bf16_of_codes(code[s].y, m2), bf16_of_codes(code[s].z, m2),
+                            bf16_of_codes(code[s].w, m2)};
+              if (120 + k > 127) {  // past bf16's largest power of two: in two steps
+                const uint32_t e1 = (uint32_t)(k - 7 + 127) << 7, e2 = e1 | (e1 << 16);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[y] = make_uint2(mul_bf16x2(o[y].x, e2), mul_bf16x2(o[y].y, e2));
+              }
+              const int r = 16 * s + r16;
+              *reinterpret_cast<uint4*>(dst + swz128(r, 2 * (c & 3))) = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
+              *reinterpret_cast<uint4*>(dst + swz128(r, 2 * (c & 3) + 1)) = make_uint4(o[2].x, o[2].y, o[3].x, o[3].y);
+            }
+            fence_proxy_async();  // the tile before the tensor cores read it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv_full + ks + w);
+          }
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ---- softmax of slot t
+    if (E4M3) reg_alloc<184>();
+    else reg_alloc<216>();
+    const int t = warp >> 2, quarter = warp & 3;
+    const int r = 32 * quarter + lane;
+    const int G = a.p.G, R = a.R;
+    const int rr = r / G, hh = r - rr * G;
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const uint32_t ts = tmem + lane_off + kColS + 128u * t;
+    const uint32_t to = tmem + lane_off + kColO + 128u * t;
+    const int window = a.p.window, sinks = a.p.sinks;
+    const float sl2 = a.scale_log2;
+    int n = 0, nx = 0;
+    uint32_t cnt = 0, odone = 0;
+    bool ok = true;
+    while (ok && cur.next(a, sg)) {
+      const int row = (sg.single ? 0 : t * R) + rr;  // in the pair
+      const bool vok = r < G * R && row < sg.rows;
+      const int qpos = vok ? sg.p0 + row : -1;
+      float mref = ninf, lh = 0.f;  // reference maximum (log2 units), sum against it
+      bool used = false;
+      for (int i = sg.i0; i < sg.i1; ++i, ++n) {
+        if (sg.single && (n & 1) != t) continue;
+        const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
+        ok = mbar_wait(info_full + n % kInfo, (uint32_t)(n / kInfo) & 1u, status);
+        const uint32_t bad = info[n % kInfo];
+        ok = ok && mbar_wait(s_full + t, cnt & 1u, status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        float sv[BLK];
+        {
+          uint32_t q[BLK / 32][32];
+#pragma unroll
+          for (int x = 0; x < BLK / 32; ++x) tc::ld_32x32b_x32(ts + 32 * x, q[x]);
+          tc::wait_ld();
+#pragma unroll
+          for (int x = 0; x < BLK / 32; ++x) {
+            tc::reg_fence(q[x]);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) sv[32 * x + y] = __uint_as_float(q[x][y]);
+          }
+        }
+        // Blocks that every row of the warp sees whole skip the masks, and with
+        // a positive scale the maximum is taken on raw scores.
+        const bool whole = kb0 + BLK - 1 <= qpos && (window == 0 || kb0 > qpos - window || kb0 + BLK <= sinks);
+        const bool fast = bad == 0 && sl2 > 0.f && __all_sync(0xffffffffu, !vok || whole);
+        float mq[4] = {ninf, ninf, ninf, ninf}, mul = sl2;
+        if (fast) {
+#pragma unroll
+          for (int x = 0; x < BLK; ++x) mq[x & 3] = fmaxf(mq[x & 3], sv[x]);
+        } else {
+          mul = 1.f;
+#pragma unroll
+          for (int x = 0; x < BLK; ++x) {
+            const int tok = kb0 + x;
+            const bool see = row_sees(qpos, tok, window, sinks) && !((bad >> (x / 16)) & 1u);
+            sv[x] = see ? sv[x] * sl2 : ninf;
+            mq[x & 3] = fmaxf(mq[x & 3], sv[x]);
+          }
+        }
+        float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        if (fast) mx *= sl2;
+        const float mn = fmaxf(mref, mx);
+        const bool upd = mn != ninf && (mref == ninf || mn > mref + 8.f);
+        const float alpha = !upd ? 1.f : (mref == ninf ? 0.f : fast_exp2(mref - mn));
+        if (upd) mref = mn;
+        lh *= alpha;
+        if (used && __any_sync(0xffffffffu, upd)) {
+          // the PV of this slot's earlier blocks came before this block's QK
+          // in the issuing thread, so O is at rest here
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t q[32];
+            tc::ld_32x32b_x32(to + 32 * c, q);
+            tc::wait_ld();
+            tc::reg_fence(q);
+            uint32_t lo[16], hi[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              lo[x] = __float_as_uint(__uint_as_float(q[x]) * alpha);
+              hi[x] = __float_as_uint(__uint_as_float(q[16 + x]) * alpha);
+            }
+            tc::st_32x32b_x16(to + 32 * c, lo);
+            tc::st_32x32b_x16(to + 32 * c + 16, hi);
+          }
+        }
+        const float nmn = mref == ninf ? 0.f : -mref;  // nothing seen so far: every p is exp2(-inf) = 0
+        float rq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h2 = 0; h2 < BLK / 32; ++h2) {
+          uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float e0 = fast_exp2(fmaf(sv[32 * h2 + 2 * j], mul, nmn));
+            const float e1 = fast_exp2(fmaf(sv[32 * h2 + 2 * j + 1], mul, nmn));
+            rq[j & 3] += e0 + e1;
+            p1[j] = pack_bf16(e0, e1);
+            if (TERMS == 3) {
+              const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
+              p2[j] = pack_bf16(d0, d1);
+              p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
+            }
+          }
+          tc::st_32x32b_x16(ts + 16 * h2, p1);
+          if constexpr (TERMS == 3) {
+            tc::st_32x32b_x16(ts + 32 + 16 * h2, p2);
+            tc::st_32x32b_x16(ts + 64 + 16 * h2, p3);
+          }
+        }
+        lh += (rq[0] + rq[1]) + (rq[2] + rq[3]);
+        // bf16 tiles hold whatever the cache has at tokens that no row of the
+        // pair sees: their V rows are zeroed before PV reads them
+        if (!E4M3 && (kb0 + BLK > sg.p1 + 1 || (kb0 < sg.lo && kb0 + BLK > sg.S))) {
+          const int vs = (2 * n) % NS + 1;
+          ok = mbar_wait(kv_full + vs, (uint32_t)((2 * n) / NS) & 1u, status);
+          unsigned char* vt = ring + vs * Sh::kSlot;
+          if (ok) {
+            for (int x = r; x < BLK * 16; x += 128) {
+              const int y = x >> 4, ch = x & 15, tok = kb0 + y;
+              if (!(tok < sg.S || (tok >= sg.lo && tok <= sg.p1)))
+                *reinterpret_cast<uint4*>(vt + (ch >> 3) * Sh::kHalf + swz128(y, ch & 7)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async();
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+        }
+        tc::wait_st();
+        tc::fence_before_sync();  // P and the rescaled O before PV reads them
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + t);
+        ++cnt;
+        used = true;
+      }
+      if (!ok) break;
+      // ---- the row's result
+      if (used) {
+        ok = mbar_wait(o_full + t, odone & 1u, status);
+        ++odone;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+      }
+      const bool whole = sg.i0 == 0 && sg.i1 == sg.nb;
+      float f0 = 1.f, f1 = 0.f;              // weights of this slot's and the other slot's result
+      const float* other = nullptr;
+      float* xrow = a.xbuf + ((size_t)blockIdx.x * 128 + r) * kChunkPart;
+      if (sg.single && sg.nb > 0) {
+        if (t == 1) {
+          if (nx > 0) ok = mbar_wait(x_empty, (nx - 1) & 1u, status);
+        } else {
+          ok = mbar_wait(x_full, nx & 1u, status);
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (t == 0) {
+          const float m1 = __ldcg(xrow + kHeadDim), l1 = __ldcg(xrow + kHeadDim + 1);
+          const float M = fmaxf(mref, m1);
+          if (M != ninf) {
+            f0 = fast_exp2(mref - M);
+            f1 = fast_exp2(m1 - M);
+          }
+          lh = lh * f0 + l1 * f1;
+          mref = M;
+          other = xrow;
+        }
+      }
+      float* part = nullptr;  // where an unnormalised result goes
+      if (sg.single && sg.nb > 0 && t == 1) {
+        part = xrow;
+      } else if (!whole) {
+        part = a.parts + ((((size_t)blockIdx.x * 2 + (sg.i0 == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart;
+      }
+      const float inv = part ? 1.f : (lh > 0.f ? 1.f / lh : 0.f);
+      const size_t orow = vok ? (size_t)(sg.row0 + row) * a.p.Hq + (size_t)sg.g * G + hh : 0;
+      const bool skip = sg.single && t == 1 && sg.nb == 0;  // slot 0 writes the zeros
+      f0 *= inv;
+      f1 *= inv;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t q[16];
+        if (used) {
+          tc::ld_32x32b_x16(to + 16 * c, q);
+          tc::wait_ld();
+          tc::reg_fence(q);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) q[x] = 0u;
+        }
+        float o[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = __uint_as_float(q[x]) * f0;
+        if (other) {
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(other + 16 * c + x));
+            o[x] += y.x * f1;
+            o[x + 1] += y.y * f1;
+            o[x + 2] += y.z * f1;
+            o[x + 3] += y.w * f1;
+          }
+        }
+        if (vok && !skip) {
+          if (part || a.p.out) {
+            float* d = (part ? part : a.p.out + orow * kHeadDim) + 16 * c;
+#pragma unroll
+            for (int x = 0; x < 16; x += 4)
+              *reinterpret_cast<float4*>(d + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          } else {
+            uint4* d = reinterpret_cast<uint4*>(a.p.out_bf16 + orow * kHeadDim + 16 * c);
+            d[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+            d[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]), pack_bf16(o[12], o[13]),
+                              pack_bf16(o[14], o[15]));
+          }
+        }
+      }
+      if (vok && !skip) {
+        if (part) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mref, lh);
+        else if (a.p.lse) a.p.lse[orow] = lh > 0.f ? mref * kLn2 + logf(lh) : ninf;
+        if (sg.i0 == 0 && qpos < 0) flag_status(status, SA_ERR_DEVICE_CHECK);
+      }
+      if (sg.single && sg.nb > 0) {
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(t == 1 ? x_full : x_empty);
+        ++nx;
+      }
+      tc::fence_before_sync();
+      if (tid == 0 && !whole && sg.i0 == 0) {
+        // the CTA that holds the pair's last block
+        const unsigned long long nc = s_plan.n_cta, total = s_plan.total, x = sg.w + sg.cost - 1;
+        unsigned long long c = x * nc / total;
+        while (c + 1 < nc && total * (c + 1) / nc <= x) ++c;
+        while (c > 0 && total * c / nc > x) --c;
+        a.recs[blockIdx.x] = ChunkRec{sg.row0, sg.rows, sg.g, (int)c, sg.single ? 1 : 0};
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// Merge of the partial results of the pairs that were cut: block x / 8 looks
+// after the pair that CTA x / 8 began, a warp after four of its 256 vectors,
+// lane l after dims 4 l .. 4 l + 3; parts in CTA order.
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ ChunkArgs a) {
+  grid_dep_wait();
+  const int c0 = blockIdx.x >> 3;
+  const ChunkRec rec = a.recs[c0];
+  if (rec.rows <= 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float ninf = -__int_as_float(0x7f800000);
+  const int G = a.p.G, R = a.R;
+  for (int i = 0; i < 4; ++i) {
+    const int v = (blockIdx.x & 7) * 32 + warp * 4 + i;
+    const int t = v >> 7, r = v & 127;
+    const int rr = r / G, row = t * R + rr;
+    if (r >= G * R || row >= rec.rows || (rec.single && t)) continue;
+    float M = ninf, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int np = rec.last - c0 + 1;
+    for (int p0 = 0; p0 < np; p0 += 32) {
+      const int p = p0 + lane;
+      float2 ml = make_float2(ninf, 0.f);
+      if (p < np)
+        ml = __ldcg(reinterpret_cast<const float2*>(
+            a.parts + ((((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart + kHeadDim));
+      float mm = ml.x;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
+      const float nm = fmaxf(M, mm);
+      if (nm == ninf) continue;
+      const float f = fast_exp2(M - nm), w = fast_exp2(ml.x - nm);
+      float lw = ml.y * w;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
+      L = L * f + lw;
+      o.x *= f;
+      o.y *= f;
+      o.z *= f;
+      o.w *= f;
+      M = nm;
+      const int cntp = min(32, np - p0);
+#pragma unroll 8
+      for (int q = 0; q < cntp; ++q) {
+        const float wq = __shfl_sync(0xffffffffu, w, q);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(
+            a.parts + ((((size_t)(c0 + p0 + q) * 2 + (p0 + q == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart + 4 * lane));
+        o.x += y.x * wq;
+        o.y += y.y * wq;
+        o.z += y.z * wq;
+        o.w += y.w * wq;
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const size_t orow = (size_t)(rec.row0 + row) * a.p.Hq + (size_t)rec.g * G + (r - rr * G);
+    if (a.p.out)
+      *reinterpret_cast<float4*>(a.p.out + orow * kHeadDim + 4 * lane) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+      *reinterpret_cast<uint2*>(a.p.out_bf16 + orow * kHeadDim + 4 * lane) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (a.p.lse && lane == 0) a.p.lse[orow] = L > 0.f ? M * kLn2 + logf(L) : ninf;
+  }
+}
+
+template <bool E4M3, int TERMS>
+cudaError_t launch(const ChunkArgs& a, int grid, cudaStream_t st) {
+  auto* k = chunk_kernel<E4M3, TERMS>;
+  const cudaError_t e = allow_smem((const void*)k, Shape<TERMS>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, (unsigned)grid, E4M3 ? 512 : 384, Shape<TERMS>::kSmem, st, a);
+}
+
+}  // namespace
+
+int chunk_block_tokens(bool fp32_out) { return fp32_out ? Shape<3>::BLK : Shape<1>::BLK; }
+
+cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st) {
+  const bool f32 = a.p.out != nullptr;
+  const cudaError_t e = a.p.kv.e4m3 ? (f32 ? launch<true, 3>(a, grid, st) : launch<true, 1>(a, grid, st))
+                                    : (f32 ? launch<false, 3>(a, grid, st) : launch<false, 1>(a, grid, st));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(combine_kernel, (unsigned)grid * 8, 256, 0, st, a);
+}
+
+}  // namespace sa

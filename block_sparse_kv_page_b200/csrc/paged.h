@@ -63,4 +63,26 @@ struct PagedAttnArgs {
 };
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t st);
 
+// Chunk attention (chunk_attn.cu).
+constexpr int kChunkPart = 128 + 4;  // floats of a partial result: acc[128], reference maximum, sum, 2 unused
+struct ChunkRec {                    // a pair cut between CTAs, kept by the CTA that holds its first block
+  int row0, rows, g, last, single;   // rows 0: none; last: the CTA that holds its last block
+};
+struct ChunkArgs {
+  CUtensorMap tmap_q;                // [n_rows][Hq][128], box R x G x 64, 128B swizzle
+  CUtensorMap tmap_k, tmap_v;        // bf16 cache: [n_pages][Hkv][page_size][128], box 1 x 1 x hb x 64
+  PagedAttnArgs p;
+  float scale_log2;                  // scale * log2(e)
+  int R;                             // rows of a tile, floor(128 / G)
+  int hb;                            // rows of a K or V box: divides page_size and the block
+  float* parts;                      // [grid][head, tail segment][slot][128][kChunkPart]
+  float* xbuf;                       // [grid][128][kChunkPart]
+  ChunkRec* recs;                    // [grid]
+};
+cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st);
+int chunk_block_tokens(bool fp32_out);
+// Opt a kernel into `bytes` of dynamic shared memory on the current device
+// (remembered per device; any thread may call it).
+cudaError_t allow_smem(const void* func, size_t bytes);
+
 }  // namespace sa
