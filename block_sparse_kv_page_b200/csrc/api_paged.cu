@@ -144,16 +144,16 @@ sa_status chunk(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   const unsigned long long qs[2] = {kHeadDim * 2, (unsigned long long)p.q_row_stride * 2};
   const unsigned qb[3] = {64, (unsigned)p.G, (unsigned)a.R};
   if (!encode_tmap_nd(&a.tmap_q, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, qd, qs, qb, true)) return SA_ERR_CUDA;
-  if (!kv.e4m3) {
-    const unsigned long long d[4] = {kHeadDim, (unsigned long long)kv.page_size, (unsigned long long)kv.Hkv,
-                                     (unsigned long long)kv.n_pages};
-    const unsigned long long s[3] = {(unsigned long long)kv.token_stride, (unsigned long long)kv.head_stride,
-                                     (unsigned long long)kv.page_stride};
-    const unsigned b[4] = {64, (unsigned)a.hb, 1, 1};
-    if (!encode_tmap_nd(&a.tmap_k, kv.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, d, s, b, true) ||
-        !encode_tmap_nd(&a.tmap_v, kv.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, d, s, b, true))
-      return SA_ERR_CUDA;
-  }
+  const unsigned long long d[4] = {kHeadDim, (unsigned long long)kv.page_size, (unsigned long long)kv.Hkv,
+                                   (unsigned long long)kv.n_pages};
+  const unsigned long long s[3] = {(unsigned long long)kv.token_stride, (unsigned long long)kv.head_stride,
+                                   (unsigned long long)kv.page_stride};
+  // bf16: halves of 64 dims, swizzled for the MMA; e4m3: whole rows of codes
+  const unsigned b[4] = {kv.e4m3 ? 128u : 64u, (unsigned)a.hb, 1, 1};
+  const CUtensorMapDataType dt = kv.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!encode_tmap_nd(&a.tmap_k, kv.k, dt, 4, d, s, b, !kv.e4m3) ||
+      !encode_tmap_nd(&a.tmap_v, kv.v, dt, 4, d, s, b, !kv.e4m3))
+    return SA_ERR_CUDA;
   const PagedScratch sc = paged_scratch();
   a.parts = (float*)(ws + sc.parts);
   a.xbuf = (float*)(ws + sc.xbuf);

@@ -24,16 +24,26 @@
 // CTA, warp-specialised, every wait bounded:
 //   warps 0-3 / 4-7  softmax of tile slot 0 / 1: thread = query vector (TMEM
 //                    lane), its whole row of BLK scores in registers;
-//   warp 8           TMA of the queries and, for a bf16 cache, of the K and V
-//                    tiles (boxes of up to BLK rows inside a page; boxes that
-//                    no row of the pair needs, or whose page is bad, are
-//                    fetched from past the pool's end and so read as zeros);
+//   warp 8           TMA of the queries and of the K and V tiles (boxes of up to
+//                    BLK rows inside a page; boxes that no row of the pair
+//                    needs, or whose page is bad, are fetched from past the
+//                    pool's end and so read as zeros);
 //   warps 9, 10      MMA issue of slot 0 / 1 (one thread each): S = Q K^T into
-//                    the slot's S columns, then, once the softmax has written
-//                    P over S, O += P V;
-//   warps 12-15      (e4m3 cache) turn the codes of K and V into bf16 tiles:
-//                    code * 2^k is exactly a bf16, so the products are those of
-//                    a bf16 cache of the rounded values.
+//                    the slot's S columns and, once the softmax has written P
+//                    over S, O += P V.  An MMA's issue returns when the tensor
+//                    pipe takes it (70 cycles each here), so whatever else one
+//                    issuing thread does adds to the products' time (1340 of
+//                    3590 cycles a block); two threads issuing at will fall into
+//                    step, both slots' softmax in turn with both slots'
+//                    products.  So each slot has a thread, which waits for its
+//                    operands first and then takes its turn: PV of the slot's
+//                    last block and QK of its next are issued as one group, the
+//                    slots' groups one after another, and one slot's softmax
+//                    runs under the other slot's products;
+//   warps 12-15      (e4m3 cache) turn the codes of K and V, fetched into a
+//                    ring of their own, into bf16 tiles: code * 2^k is exactly
+//                    a bf16, so the products are those of a bf16 cache of the
+//                    rounded values.
 // Roles run ahead of each other over block and segment boundaries; only the
 // mbarriers order them.
 //
@@ -54,6 +64,10 @@ constexpr int kQTileBytes = 2 * 128 * 128;
 constexpr int kRingBytes = 128 * 1024;
 constexpr uint32_t kColS = 0, kColO = 256;  // slot t: S / P at 128 t, O at 256 + 128 t
 
+#ifndef SA_CHUNK_PARTS
+#define SA_CHUNK_PARTS 1
+#endif
+
 template <int TERMS>
 struct Shape {
   static constexpr int BLK = TERMS == 1 ? 128 : 64;   // tokens of a block
@@ -61,10 +75,19 @@ struct Shape {
   static constexpr int kSlot = 2 * kHalf;             // a K or V tile
   static constexpr int NS = kRingBytes / kSlot;       // ring slots (K, V alternating)
   static constexpr int kOffRing = 2 * kQTileBytes;
-  static constexpr int kOffBars = kOffRing + kRingBytes;
-  static constexpr int kNumBars = 2 * NS + 2 + 6 + kInfo + 2 + 1;
-  static constexpr int kOffInfo = kOffBars + 8 * kNumBars;
-  static constexpr int kSmem = 1024 + kOffInfo + 4 * kInfo + 16;
+  static constexpr int kRaw = BLK * 128;              // codes of a K or V tile
+  static constexpr int kOffRaw = kOffRing + kRingBytes;   // e4m3 only: two tiles of codes
+  static constexpr int kParts = SA_CHUNK_PARTS;       // P is handed over in so many parts
+  static constexpr int kNumBars = 2 * NS + 2 + 4 + 2 * kParts + kInfo + 2 + 1 + 4;
+  static constexpr int off_bars(bool e4m3) { return kOffRaw + (e4m3 ? 2 * kRaw : 0); }
+  static constexpr int off_info(bool e4m3) { return off_bars(e4m3) + 8 * kNumBars; }
+  static constexpr int off_scale(bool e4m3) { return (off_info(e4m3) + 4 * (kInfo + 1) + 15) & ~15; }
+  static constexpr int smem(bool e4m3) { return 1024 + off_scale(e4m3) + (e4m3 ? 2 * BLK : 0); }
+};
+
+template <bool B>
+struct BoolTag {
+  static constexpr bool value = B;
 };
 
 template <int R>
@@ -307,6 +330,56 @@ SA_DEV uint2 bf16_of_codes(uint32_t w, uint32_t m2) {
   return make_uint2(prmt(even, odd, 0x5410), prmt(even, odd, 0x7632));
 }
 
+// Two fp32 values in one 64-bit register pair, for the packed instructions.
+SA_DEV unsigned long long pack_f2(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+SA_DEV void unpack_f2(unsigned long long v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(v));
+}
+SA_DEV unsigned long long fma_f2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+SA_DEV unsigned long long add_f2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SA_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 2^x of two finite values on the FMA pipe: x = n + f with n the nearest whole
+// number (by adding and subtracting 1.5 * 2^23) and |f| <= 1/2, 2^f by the
+// degree-4 polynomial of least relative error there (Remez exchange; 2.6e-6),
+// n added to its exponent.  The special-function unit gives 16 exponentials a
+// clock and SM, which by itself would take as long as both matrix products.
+SA_DEV unsigned long long poly_exp2(float x, float y) {
+  const unsigned long long magic = pack_f2(12582912.f, 12582912.f), nmagic = pack_f2(-12582912.f, -12582912.f);
+  const unsigned long long v = pack_f2(fmaxf(x, -126.f), fmaxf(y, -126.f));
+  const unsigned long long r = add_f2(v, magic);
+  const unsigned long long f = fma_f2(add_f2(r, nmagic), pack_f2(-1.f, -1.f), v);
+  unsigned long long p = fma_f2(pack_f2(9.570101911e-03f, 9.570101911e-03f), f, pack_f2(5.591786032e-02f, 5.591786032e-02f));
+  p = fma_f2(p, f, pack_f2(2.402474483e-01f, 2.402474483e-01f));
+  p = fma_f2(p, f, pack_f2(6.931218147e-01f, 6.931218147e-01f));
+  p = fma_f2(p, f, pack_f2(9.999992614e-01f, 9.999992614e-01f));
+  float r0, r1, p0, p1;
+  unpack_f2(r, r0, r1);
+  unpack_f2(p, p0, p1);
+  return pack_f2(__uint_as_float((__float_as_uint(r0) << 23) + __float_as_uint(p0)),
+                 __uint_as_float((__float_as_uint(r1) << 23) + __float_as_uint(p1)));
+}
+#ifndef SA_CHUNK_POLY
+#define SA_CHUNK_POLY 5
+#endif
+constexpr int kPoly = SA_CHUNK_POLY;  // of 16 pairs of exponentials, those taken by poly_exp2
+
 template <bool E4M3, int TERMS>
 __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using Sh = Shape<TERMS>;
@@ -319,18 +392,23 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* qs = base;
   unsigned char* ring = base + Sh::kOffRing;
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(base + Sh::kOffBars);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(base + Sh::off_bars(E4M3));
   uint64_t* kv_empty = kv_full + NS;
   uint64_t* q_full = kv_empty + NS;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;   // [slot]
-  uint64_t* p_full = s_full + 2;    // [slot]
-  uint64_t* o_full = p_full + 2;    // [slot]
-  uint64_t* info_full = o_full + 2;
+  uint64_t* o_full = s_full + 2;    // [slot]
+  uint64_t* p_full = o_full + 2;    // [slot][part]
+  uint64_t* info_full = p_full + 2 * Sh::kParts;
   uint64_t* x_full = info_full + kInfo;
   uint64_t* x_empty = x_full + 1;
   uint64_t* drain = x_empty + 1;
-  volatile uint32_t* info = reinterpret_cast<uint32_t*>(base + Sh::kOffInfo);
+  uint64_t* raw_full = drain + 1;   // [2]
+  uint64_t* raw_empty = raw_full + 2;
+  volatile uint32_t* info = reinterpret_cast<uint32_t*>(base + Sh::off_info(E4M3));
+  volatile uint32_t* turn = info + kInfo;  // MMA groups issued so far
+  unsigned char* raw = base + Sh::kOffRaw;
+  unsigned char* raw_scale = base + Sh::off_scale(E4M3);  // [2][BLK]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float ninf = -__int_as_float(0x7f800000);
@@ -343,21 +421,22 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
+    *turn = 0u;
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full + t, 1);
-      mbar_init(p_full + t, 4);
       mbar_init(o_full + t, 1);
+      mbar_init(raw_full + t, 1);
+      mbar_init(raw_empty + t, 4);
     }
+    for (int i = 0; i < 2 * Sh::kParts; ++i) mbar_init(p_full + i, 4);
     for (int i = 0; i < kInfo; ++i) mbar_init(info_full + i, 1);
     mbar_init(x_full, 4);
     mbar_init(x_empty, 4);
     mbar_init(drain, 2);
     fence_barrier_init();
     prefetch_tmap(&a.tmap_q);
-    if (!E4M3) {
-      prefetch_tmap(&a.tmap_k);
-      prefetch_tmap(&a.tmap_v);
-    }
+    prefetch_tmap(&a.tmap_k);
+    prefetch_tmap(&a.tmap_v);
   }
   if (warp == 0) {
     tc::tmem_alloc(&s_tmem, 512);
@@ -379,7 +458,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
     else reg_dealloc<72>();
     if (warp == 8) {
       // ---- producer
-      int n = 0, segs = 0;
+      int n = 0, segs = 0, issued = 0;  // issued: K and V tiles
       bool ok = true;
       const int hb = a.hb, nbox = BLK / hb;
       while (ok && cur.next(a, sg)) {
@@ -413,104 +492,156 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
             }
           }
           bad = __reduce_or_sync(0xffffffffu, bad);
-          const int ks = (2 * n) % NS, vs = ks + 1;
+          const int ks = (2 * n) % NS;
           const uint32_t use = (uint32_t)((2 * n) / NS);
-          if (use > 0) ok = mbar_wait(kv_empty + ks, (use - 1) & 1u, status);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            info[n % kInfo] = bad;
-            mbar_arrive(info_full + n % kInfo);
-          }
-          if (!E4M3) {
-            const int at = page < 0 ? (int)kv.n_pages : page;  // past the pool: zeros
-            if (lane == 0) mbar_arrive_expect_tx(kv_full + ks, Sh::kSlot);
-            __syncwarp();
-            if (sub < nbox)
-              tma_load_4d(ring + ks * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128, &a.tmap_k, 64 * (lane & 1),
-                          slot, sg.g, at, kv_full + ks);
-            if (use > 0) ok = mbar_wait(kv_empty + vs, (use - 1) & 1u, status);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              ++n;  // the K tile was issued
-              break;
+          const int at = page < 0 ? (int)kv.n_pages : page;  // past the pool: zeros
+          if (E4M3) {
+            // codes of K, then of V, with their rows' scale bytes
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0 && !(lane & 1)));
+            for (int w = 0; w < 2; ++w) {
+              if (n > 0) ok = mbar_wait(raw_empty + w, (n - 1) & 1u, status);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              if (w == 0 && lane == 0) {
+                info[n % kInfo] = bad;
+                mbar_arrive(info_full + n % kInfo);
+              }
+              if (lane == 0) mbar_arrive_expect_tx(raw_full + w, (uint32_t)Sh::kRaw + boxes * hb);
+              __syncwarp();
+              if (sub < nbox && !(lane & 1)) {
+                tma_load_4d(raw + w * Sh::kRaw + sub * hb * 128, w ? &a.tmap_v : &a.tmap_k, 0, slot, sg.g, at,
+                            raw_full + w);
+                if (page >= 0)
+                  bulk_load(raw_scale + w * BLK + sub * hb,
+                            (w ? kv.v_scale : kv.k_scale) + scale_index(kv, page, sg.g, slot), hb, raw_full + w);
+              }
+              issued = 2 * n + w + 1;
             }
-            if (lane == 0) mbar_arrive_expect_tx(kv_full + vs, Sh::kSlot);
-            __syncwarp();
-            if (sub < nbox)
-              tma_load_4d(ring + vs * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128, &a.tmap_v, 64 * (lane & 1),
-                          slot, sg.g, at, kv_full + vs);
+            if (!ok) break;
+          } else {
+            for (int w = 0; w < 2; ++w) {
+              if (use > 0) ok = mbar_wait(kv_empty + ks + w, (use - 1) & 1u, status);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              if (w == 0 && lane == 0) {
+                info[n % kInfo] = bad;
+                mbar_arrive(info_full + n % kInfo);
+              }
+              if (lane == 0) mbar_arrive_expect_tx(kv_full + ks + w, Sh::kSlot);
+              __syncwarp();
+              if (sub < nbox)
+                tma_load_4d(ring + (ks + w) * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128,
+                            w ? &a.tmap_v : &a.tmap_k, 64 * (lane & 1), slot, sg.g, at, kv_full + ks + w);
+              issued = 2 * n + w + 1;
+            }
+            if (!ok) break;
           }
         }
       }
       // every copy issued has landed before the CTA ends (bounded)
       if (segs > 0) mbar_wait(q_full, (segs - 1) & 1u, nullptr);
-      if (!E4M3) {
-        for (int x = max(0, n - NS / 2); x < n; ++x) {
-          mbar_wait(kv_full + (2 * x) % NS, ((2 * x) / NS) & 1u, nullptr);
-          if (ok) mbar_wait(kv_full + (2 * x) % NS + 1, ((2 * x) / NS) & 1u, nullptr);
-        }
+      if (E4M3) {
+        for (int x = max(0, issued - 2); x < issued; ++x) mbar_wait(raw_full + (x & 1), (x >> 1) & 1u, nullptr);
+      } else {
+        for (int x = max(0, issued - NS); x < issued; ++x) mbar_wait(kv_full + x % NS, (x / NS) & 1u, nullptr);
       }
     } else if (warp < 11 && lane == 0) {
-      // ---- MMA issue of slot t
+      // ---- MMA issue of slot t.  Item k of a segment is block n0 + k of slot
+      // t (two tiles: every block, both slots in turn; one tile: every other
+      // block); its group is the PV of the slot's item before it and its QK.  A
+      // segment ends with the last items' PVs, a group each.  Groups are
+      // numbered over the whole CTA and issued in that order.
       const int t = warp - 9;
       const uint32_t idesc_s = tc::idesc_f32acc(tc::kFmtBF16, 128, BLK);
       const uint32_t idesc_o = tc::idesc_f32acc(tc::kFmtBF16, 128, kHeadDim) | (1u << 16);  // V MN-major
       const uint32_t ts = tmem + kColS + 128u * t, to = tmem + kColO + 128u * t;
+      const uint64_t k_desc = tc::smem_desc_sw128(ring), vt_desc = v_desc<Sh::kHalf>(ring);
       int n = 0, segs = 0;
-      uint32_t cnt = 0;
+      uint32_t cnt = 0, order = 0;  // PVs issued by this slot; groups of both before the segment
       bool ok = true;
-      while (ok && cur.next(a, sg)) {
-        if (sg.i0 == sg.i1) continue;
-        const int n_end = n + sg.i1 - sg.i0;
-        const int step = sg.single ? 2 : 1;
-        int last = sg.single ? n_end - 1 - (((n_end - 1) & 1) ^ t) : n_end - 1;  // this slot's last block
-        if (last < n) last = -1;
-        if (!(ok = mbar_wait(q_full, segs & 1u, status))) break;
-        tc::fence_after_sync();
-        ++segs;
-        if (last < 0) mbar_arrive(q_empty);
-        const unsigned char* qt = qs + (sg.single ? 0 : t * kQTileBytes);
-        bool first = true;
-        for (; n < n_end; ++n) {
-          const int ks = (2 * n) % NS, vs = ks + 1;
-          const uint32_t ph = (uint32_t)((2 * n) / NS) & 1u;
-          if (!(ok = mbar_wait(kv_full + ks, ph, status))) break;
-          if (step == 2 && (n & 1) != t) {  // the other slot's block
-            mbar_arrive(kv_empty + ks);
-            if (!(ok = mbar_wait(kv_full + vs, ph, status))) break;
-            mbar_arrive(kv_empty + vs);
-            continue;
+      // (a count, not a barrier: a slot may sit out any number of groups, and a
+      // barrier's parity tells only neighbouring phases apart)
+      auto my_turn = [&](uint32_t g) -> bool {
+        for (uint32_t i = 0; i < kSpinLimit; ++i)
+          if (*turn == g) return true;
+        flag_status(status, SA_ERR_TIMEOUT);
+        return false;
+      };
+      // P and V of block m have come
+      auto pv_ready = [&](int m) -> bool {
+        return mbar_wait(kv_full + (2 * m) % NS + 1, (uint32_t)((2 * m) / NS) & 1u, status) &&
+               mbar_wait(p_full + t * Sh::kParts, cnt & 1u, status);
+      };
+      auto pv = [&](int m, bool first, bool twice) -> bool {
+        const int vs = (2 * m) % NS + 1;
+        const uint64_t vd = vt_desc + (uint64_t)(vs * (Sh::kSlot >> 4));
+        constexpr int kSteps = BLK / 16 / Sh::kParts;
+#pragma unroll
+        for (int part = 0; part < Sh::kParts; ++part) {
+          if (part > 0) {
+            if (!mbar_wait(p_full + t * Sh::kParts + part, cnt & 1u, status)) return false;
+            tc::fence_after_sync();
           }
-          tc::fence_after_sync();
-          const unsigned char* kt = ring + ks * Sh::kSlot;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_bf16_ss(ts, tc::smem_desc_sw128(qt + c * (128 * 128) + 32 * k),
-                              tc::smem_desc_sw128(kt + c * Sh::kHalf + 32 * k), idesc_s, (c | k) != 0);
-          tc::commit(s_full + t);
-          tc::commit(kv_empty + ks);
-          if (n == last) tc::commit(q_empty);
-          if (!(ok = mbar_wait(kv_full + vs, ph, status))) break;
-          if (!(ok = mbar_wait(p_full + t, cnt & 1u, status))) break;
-          tc::fence_after_sync();
-          ++cnt;
-          const unsigned char* vt = ring + vs * Sh::kSlot;
 #pragma unroll
           for (int x = 0; x < TERMS; ++x)
 #pragma unroll
-            for (int j = 0; j < BLK / 16; ++j)
-              tc::mma_bf16_ts(to, ts + (uint32_t)(x * (BLK / 2) + 8 * j), v_desc<Sh::kHalf>(vt + 16 * 128 * j), idesc_o,
+            for (int j = part * kSteps; j < (part + 1) * kSteps; ++j)
+              tc::mma_bf16_ts(to, ts + (uint32_t)(x * (BLK / 2) + 8 * j), vd + (uint64_t)(128 * j), idesc_o,
                               !first || (x | j) != 0);
-          first = false;
-          tc::commit(kv_empty + vs);
-          if (n == last) tc::commit(o_full + t);
+        }
+        ++cnt;
+        tc::commit(kv_empty + vs);
+        if (twice) tc::commit(kv_empty + vs);  // the other slot has no part in this block
+        return true;
+      };
+      while (ok && cur.next(a, sg)) {
+        const int nblk = sg.i1 - sg.i0, n0 = n;
+        if (nblk == 0) continue;
+        const bool single = sg.single;
+        n += nblk;
+        if (!(ok = mbar_wait(q_full, segs & 1u, status))) break;
+        ++segs;
+        const int step = single ? 2 : 1;
+        const int k0 = single ? (n0 ^ t) & 1 : 0;  // this slot's first item
+        const uint64_t q_desc = tc::smem_desc_sw128(qs + (single ? 0 : t * kQTileBytes));
+        if (k0 >= nblk) mbar_arrive(q_empty);
+        int k = k0;
+        for (; k < nblk; k += step) {
+          const int m = n0 + k, ks = (2 * m) % NS;
+          if (!(ok = mbar_wait(kv_full + ks, (uint32_t)((2 * m) / NS) & 1u, status))) break;
+          if (k > k0 && !(ok = pv_ready(m - step))) break;
+          if (!(ok = my_turn(order + (single ? k : 2 * k + t)))) break;
+          tc::fence_after_sync();
+          if (k > k0 && !(ok = pv(m - step, k == k0 + step, single))) break;
+          const uint64_t kd = k_desc + (uint64_t)(ks * (Sh::kSlot >> 4));
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              tc::mma_bf16_ss(ts, q_desc + (uint64_t)(c * (128 * 128 / 16) + 2 * x),
+                              kd + (uint64_t)(c * (Sh::kHalf / 16) + 2 * x), idesc_s, (c | x) != 0);
+          *turn = *turn + 1u;
+          tc::commit(s_full + t);
+          tc::commit(kv_empty + ks);
+          if (single) tc::commit(kv_empty + ks);
+          if (k + step >= nblk) tc::commit(q_empty);
         }
         if (!ok) break;
+        if (k > k0) {
+          const int last = k - step;  // this slot's last item
+          const uint32_t g = single ? (uint32_t)(nblk + (nblk >= 2 && last == nblk - 1 ? 1 : 0)) : (uint32_t)(2 * nblk + t);
+          if (!(ok = pv_ready(n0 + last))) break;
+          if (!(ok = my_turn(order + g))) break;
+          tc::fence_after_sync();
+          if (!(ok = pv(n0 + last, last == k0, single))) break;
+          *turn = *turn + 1u;
+          tc::commit(o_full + t);
+        }
+        order += (uint32_t)(single ? nblk + min(nblk, 2) : 2 * nblk + 2);
       }
       // every MMA issued has completed before TMEM is freed (bounded)
       tc::commit(drain);
@@ -518,7 +649,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
     }
   } else if (warp >= 12) {
     // ---- e4m3 -> bf16: 8 threads per row, 16 rows at a time
-    if (E4M3) {
+    if constexpr (E4M3) {
       reg_dealloc<88>();
       const int x = tid - 384, c = x & 7, r16 = x >> 3;
       int n = 0;
@@ -526,31 +657,33 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
       while (ok && cur.next(a, sg)) {
         for (int i = sg.i0; ok && i < sg.i1; ++i, ++n) {
           const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
+          // rows that no row of the pair sees become zeros, whatever they hold
+          const bool edge = kb0 + BLK > sg.p1 + 1 || (kb0 < sg.lo && kb0 + BLK > sg.S);
           const int ks = (2 * n) % NS;
           const uint32_t use = (uint32_t)((2 * n) / NS);
-          long long off[BLK / 16];
-          uint32_t sc[BLK / 16];  // K scale | V scale << 8
-#pragma unroll
-          for (int s = 0; s < BLK / 16; ++s) {
-            const int t = kb0 + 16 * s + r16;
-            off[s] = -1;
-            sc[s] = 0;
-            if (t < sg.S || (t >= sg.lo && t <= sg.p1)) {
-              const int p = t / kv.page_size, slot = t - p * kv.page_size;
-              const int page = paged_page(kv, sg.b, p, nullptr);
-              if (page >= 0) {
-                off[s] = paged_offset(kv, page, sg.g, slot) + 16 * c;
-                const size_t at = scale_index(kv, page, sg.g, slot);
-                sc[s] = (uint32_t)__ldg(kv.k_scale + at) | ((uint32_t)__ldg(kv.v_scale + at) << 8);
-              }
-            }
-          }
 #pragma unroll 1
           for (int w = 0; w < 2 && ok; ++w) {
+            ok = mbar_wait(raw_full + w, n & 1u, status);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
             uint4 code[BLK / 16];
+            uint32_t sc[BLK / 16];
 #pragma unroll
-            for (int s = 0; s < BLK / 16; ++s)
-              code[s] = off[s] >= 0 ? ldg_nc128((w ? kv.v : kv.k) + off[s]) : make_uint4(0u, 0u, 0u, 0u);
+            for (int s = 0; s < BLK / 16; ++s) {
+              code[s] = lds128(raw + w * Sh::kRaw + (16 * s + r16) * 128 + 16 * c);
+              sc[s] = raw_scale[w * BLK + 16 * s + r16];
+            }
+            if (edge) {
+#pragma unroll
+              for (int s = 0; s < BLK / 16; ++s) {
+                const int tok = kb0 + 16 * s + r16;
+                if (!(tok < sg.S || (tok >= sg.lo && tok <= sg.p1))) code[s] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_empty + w);
             if (use > 0) ok = mbar_wait(kv_empty + ks + w, (use - 1) & 1u, status);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
@@ -559,7 +692,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
             unsigned char* dst = ring + (ks + w) * Sh::kSlot + (c >> 2) * Sh::kHalf;
 #pragma unroll
             for (int s = 0; s < BLK / 16; ++s) {
-              const int k = (int)((sc[s] >> (8 * w)) & 255u) - 127;  // the row's scale is 2^k
+              const int k = (int)sc[s] - 127;  // the row's scale is 2^k
               const uint32_t m1 = (uint32_t)(min(max(120 + k, -126), 127) + 127) << 7;
               const uint32_t m2 = m1 | (m1 << 16);
               uint2 o[4] = {bf16_of_codes(code[s].x, m2), bf16_of_codes(code[s].y, m2), bf16_of_codes(code[s].z, m2),
@@ -633,7 +766,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         float mq[4] = {ninf, ninf, ninf, ninf}, mul = sl2;
         if (fast) {
 #pragma unroll
-          for (int x = 0; x < BLK; ++x) mq[x & 3] = fmaxf(mq[x & 3], sv[x]);
+          for (int x = 0; x < BLK; x += 2) mq[(x >> 1) & 3] = max3(mq[(x >> 1) & 3], sv[x], sv[x + 1]);
         } else {
           mul = 1.f;
 #pragma unroll
@@ -652,8 +785,8 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         if (upd) mref = mn;
         lh *= alpha;
         if (used && __any_sync(0xffffffffu, upd)) {
-          // the PV of this slot's earlier blocks came before this block's QK
-          // in the issuing thread, so O is at rest here
+          // this slot's earlier PVs came before this block's QK in the issuing
+          // thread, so O is at rest here
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t q[32];
@@ -671,29 +804,6 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
           }
         }
         const float nmn = mref == ninf ? 0.f : -mref;  // nothing seen so far: every p is exp2(-inf) = 0
-        float rq[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h2 = 0; h2 < BLK / 32; ++h2) {
-          uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float e0 = fast_exp2(fmaf(sv[32 * h2 + 2 * j], mul, nmn));
-            const float e1 = fast_exp2(fmaf(sv[32 * h2 + 2 * j + 1], mul, nmn));
-            rq[j & 3] += e0 + e1;
-            p1[j] = pack_bf16(e0, e1);
-            if (TERMS == 3) {
-              const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
-              p2[j] = pack_bf16(d0, d1);
-              p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
-            }
-          }
-          tc::st_32x32b_x16(ts + 16 * h2, p1);
-          if constexpr (TERMS == 3) {
-            tc::st_32x32b_x16(ts + 32 + 16 * h2, p2);
-            tc::st_32x32b_x16(ts + 64 + 16 * h2, p3);
-          }
-        }
-        lh += (rq[0] + rq[1]) + (rq[2] + rq[3]);
         // bf16 tiles hold whatever the cache has at tokens that no row of the
         // pair sees: their V rows are zeroed before PV reads them
         if (!E4M3 && (kb0 + BLK > sg.p1 + 1 || (kb0 < sg.lo && kb0 + BLK > sg.S))) {
@@ -713,10 +823,57 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
             break;
           }
         }
-        tc::wait_st();
-        tc::fence_before_sync();  // P and the rescaled O before PV reads them
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + t);
+        unsigned long long rq[2] = {0ull, 0ull};  // partial sums, two values each
+        const unsigned long long mul2 = pack_f2(mul, mul), nmn2 = pack_f2(nmn, nmn);
+        // P of 32 tokens; POLY: kPoly of 16 pairs on the FMA pipe (all finite)
+        auto exps = [&](auto poly, const int h2) {
+          uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float e0, e1;
+            unpack_f2(fma_f2(pack_f2(sv[32 * h2 + 2 * j], sv[32 * h2 + 2 * j + 1]), mul2, nmn2), e0, e1);
+            unsigned long long e;
+            if (decltype(poly)::value && (j + 1) * kPoly / 16 != j * kPoly / 16) {
+              e = poly_exp2(e0, e1);
+              unpack_f2(e, e0, e1);
+            } else {
+              e0 = fast_exp2(e0);
+              e1 = fast_exp2(e1);
+              e = pack_f2(e0, e1);
+            }
+            rq[j & 1] = add_f2(rq[j & 1], e);
+            p1[j] = pack_bf16(e0, e1);
+            if (TERMS == 3) {
+              const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
+              p2[j] = pack_bf16(d0, d1);
+              p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
+            }
+          }
+          tc::st_32x32b_x16(ts + 16 * h2, p1);
+          if constexpr (TERMS == 3) {
+            tc::st_32x32b_x16(ts + 32 + 16 * h2, p2);
+            tc::st_32x32b_x16(ts + 64 + 16 * h2, p3);
+          }
+        };
+#pragma unroll
+        for (int part = 0; part < Sh::kParts; ++part) {
+          constexpr int kPer = BLK / 32 / Sh::kParts;
+          if (TERMS == 1 && fast) {
+#pragma unroll
+            for (int h2 = part * kPer; h2 < (part + 1) * kPer; ++h2) exps(BoolTag<true>{}, h2);
+          } else {
+#pragma unroll
+            for (int h2 = part * kPer; h2 < (part + 1) * kPer; ++h2) exps(BoolTag<false>{}, h2);
+          }
+          tc::wait_st();
+          tc::fence_before_sync();  // P and the rescaled O before PV reads them
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + t * Sh::kParts + part);
+        }
+        float s0, s1, s2, s3;
+        unpack_f2(rq[0], s0, s1);
+        unpack_f2(rq[1], s2, s3);
+        lh += (s0 + s1) + (s2 + s3);
         ++cnt;
         used = true;
       }
@@ -900,9 +1057,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ch
 template <bool E4M3, int TERMS>
 cudaError_t launch(const ChunkArgs& a, int grid, cudaStream_t st) {
   auto* k = chunk_kernel<E4M3, TERMS>;
-  const cudaError_t e = allow_smem((const void*)k, Shape<TERMS>::kSmem);
+  constexpr int smem = Shape<TERMS>::smem(E4M3);
+  static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+  const cudaError_t e = allow_smem((const void*)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, (unsigned)grid, E4M3 ? 512 : 384, Shape<TERMS>::kSmem, st, a);
+  return launch_pdl(k, (unsigned)grid, E4M3 ? 512 : 384, smem, st, a);
 }
 
 }  // namespace

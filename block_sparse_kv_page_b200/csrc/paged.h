@@ -70,7 +70,8 @@ struct ChunkRec {                    // a pair cut between CTAs, kept by the CTA
 };
 struct ChunkArgs {
   CUtensorMap tmap_q;                // [n_rows][Hq][128], box R x G x 64, 128B swizzle
-  CUtensorMap tmap_k, tmap_v;        // bf16 cache: [n_pages][Hkv][page_size][128], box 1 x 1 x hb x 64
+  CUtensorMap tmap_k, tmap_v;        // [n_pages][Hkv][page_size][128], box 1 x 1 x hb x 64 (bf16, 128B
+                                     // swizzle) or x 128 (codes)
   PagedAttnArgs p;
   float scale_log2;                  // scale * log2(e)
   int R;                             // rows of a tile, floor(128 / G)
