@@ -135,7 +135,7 @@ sa_status check_heads(const sa_paged_desc* kv, int n_q_heads, int* G) {
 sa_status chunk(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   ChunkArgs a{};
   const PagedView& kv = p.kv;
-  const int blk = chunk_block_tokens(p.out != nullptr);
+  const int blk = chunk_block_tokens();
   a.p = p;
   a.scale_log2 = p.scale * kLog2e;
   a.R = 128 / p.G;

@@ -24,22 +24,19 @@
 // CTA, warp-specialised, every wait bounded:
 //   warps 0-3 / 4-7  softmax of tile slot 0 / 1: thread = query vector (TMEM
 //                    lane), its whole row of BLK scores in registers;
-//   warp 8           TMA of the queries and of the K and V tiles (boxes of up to
+//   warps 8, 11      TMA of the queries and K tiles, of the V tiles (boxes of up to
 //                    BLK rows inside a page; boxes that no row of the pair
 //                    needs, or whose page is bad, are fetched from past the
 //                    pool's end and so read as zeros);
 //   warps 9, 10      MMA issue of slot 0 / 1 (one thread each): S = Q K^T into
-//                    the slot's S columns and, once the softmax has written P
-//                    over S, O += P V.  An MMA's issue returns when the tensor
-//                    pipe takes it (70 cycles each here), so whatever else one
-//                    issuing thread does adds to the products' time (1340 of
-//                    3590 cycles a block); two threads issuing at will fall into
-//                    step, both slots' softmax in turn with both slots'
-//                    products.  So each slot has a thread, which waits for its
-//                    operands first and then takes its turn: PV of the slot's
-//                    last block and QK of its next are issued as one group, the
-//                    slots' groups one after another, and one slot's softmax
-//                    runs under the other slot's products;
+//                    one of the slot's two S buffers and, once the softmax has
+//                    written P over S, O += P V.  The order of a slot is PV of
+//                    block n - 2, QK of block n, so the softmax always finds
+//                    the next scores ready and the products of one block run
+//                    under the softmax of the next.  (With one buffer of 128
+//                    tokens a slot's softmax and products alternate, and the
+//                    loop was bound by that chain's latency: 5080 cycles per
+//                    128 tokens and pair against 2240 of MMA time.)
 //   warps 12-15      (e4m3 cache) turn the codes of K and V, fetched into a
 //                    ring of their own, into bf16 tiles: code * 2^k is exactly
 //                    a bf16, so the products are those of a bf16 cache of the
@@ -49,7 +46,7 @@
 //
 // P is rounded to bf16 where the output is bf16 (its error, 2^-9 per weight, is
 // that of the output's own rounding); for fp32 outputs it is split into three
-// bf16 terms (24 bits) on blocks of 64 tokens.
+// bf16 terms (24 bits), which leaves room for one S buffer per slot.
 #include "paged.cuh"
 #include "tcgen05.cuh"
 #include "internal.h"
@@ -59,35 +56,27 @@ namespace {
 
 constexpr int kC0 = 2;              // cost of starting a pair, in blocks
 constexpr int kMinShare = 4 + kC0;  // least work of a CTA
-constexpr int kInfo = 8;
+constexpr int kInfo = 16;
+constexpr int BLK = 64;             // tokens of a block
+constexpr int NR = 4;               // tiles of codes in flight (K, V alternating)
 constexpr int kQTileBytes = 2 * 128 * 128;
 constexpr int kRingBytes = 128 * 1024;
 constexpr uint32_t kColS = 0, kColO = 256;  // slot t: S / P at 128 t, O at 256 + 128 t
 
-#ifndef SA_CHUNK_PARTS
-#define SA_CHUNK_PARTS 1
-#endif
-
 template <int TERMS>
 struct Shape {
-  static constexpr int BLK = TERMS == 1 ? 128 : 64;   // tokens of a block
+  static constexpr int NB = TERMS == 1 ? 2 : 1;       // S buffers of a slot
   static constexpr int kHalf = BLK * 128;             // 64 dims of a tile
   static constexpr int kSlot = 2 * kHalf;             // a K or V tile
   static constexpr int NS = kRingBytes / kSlot;       // ring slots (K, V alternating)
   static constexpr int kOffRing = 2 * kQTileBytes;
   static constexpr int kRaw = BLK * 128;              // codes of a K or V tile
-  static constexpr int kOffRaw = kOffRing + kRingBytes;   // e4m3 only: two tiles of codes
-  static constexpr int kParts = SA_CHUNK_PARTS;       // P is handed over in so many parts
-  static constexpr int kNumBars = 2 * NS + 2 + 4 + 2 * kParts + kInfo + 2 + 1 + 4;
-  static constexpr int off_bars(bool e4m3) { return kOffRaw + (e4m3 ? 2 * kRaw : 0); }
+  static constexpr int kOffRaw = kOffRing + kRingBytes;   // e4m3 only: NR tiles of codes
+  static constexpr int kNumBars = 2 * NS + 2 + 2 * 6 + kInfo + 2 + 1 + 2 * NR;
+  static constexpr int off_bars(bool e4m3) { return kOffRaw + (e4m3 ? NR * kRaw : 0); }
   static constexpr int off_info(bool e4m3) { return off_bars(e4m3) + 8 * kNumBars; }
-  static constexpr int off_scale(bool e4m3) { return (off_info(e4m3) + 4 * (kInfo + 1) + 15) & ~15; }
-  static constexpr int smem(bool e4m3) { return 1024 + off_scale(e4m3) + (e4m3 ? 2 * BLK : 0); }
-};
-
-template <bool B>
-struct BoolTag {
-  static constexpr bool value = B;
+  static constexpr int off_scale(bool e4m3) { return (off_info(e4m3) + 4 * kInfo + 15) & ~15; }
+  static constexpr int smem(bool e4m3) { return 1024 + off_scale(e4m3) + (e4m3 ? NR * BLK : 0); }
 };
 
 template <int R>
@@ -116,7 +105,6 @@ SA_DEV uint64_t v_desc(const unsigned char* v) {
 struct Geom {
   int rows, p0, p1, lo, S, sb, wb0, nb;
 };
-template <int BLK>
 SA_DEV Geom pair_geom(const ChunkArgs& a, int N, int m, int j) {
   Geom q;
   q.rows = min(2 * a.R, m - 2 * a.R * j);
@@ -148,7 +136,6 @@ struct Plan {
 };
 
 // Walks the segments of a CTA; every role has its own.
-template <int BLK>
 struct Cursor {
   int b, g, j, off, N, m, r0, pairs;
   unsigned long long w, rem;
@@ -168,7 +155,7 @@ struct Cursor {
   }
   SA_DEV bool next(const ChunkArgs& a, Seg& s) {
     while (rem && b < a.p.kv.B) {
-      static_cast<Geom&>(s) = pair_geom<BLK>(a, N, m, j);
+      static_cast<Geom&>(s) = pair_geom(a, N, m, j);
       s.cost = s.nb + kC0;
       const int take = (int)min(rem, (unsigned long long)(s.cost - off));
       const int from = off, to = off + take;
@@ -200,7 +187,6 @@ struct Cursor {
 };
 
 // Work of the sequences b (one per thread of a converged warp), one KV head.
-template <int BLK>
 SA_DEV unsigned long long seq_work(const ChunkArgs& a, int b) {
   int N = 0, m = 0, r0;
   if (b < a.p.kv.B) {
@@ -210,7 +196,7 @@ SA_DEV unsigned long long seq_work(const ChunkArgs& a, int b) {
   const int pairs = (m + 2 * a.R - 1) / (2 * a.R);
   unsigned long long w = 0;
   if (pairs <= 8)
-    for (int j = 0; j < pairs; ++j) w += pair_geom<BLK>(a, N, m, j).nb + kC0;
+    for (int j = 0; j < pairs; ++j) w += pair_geom(a, N, m, j).nb + kC0;
   unsigned many = __ballot_sync(0xffffffffu, pairs > 8);  // long ones: the whole warp
   const int lane = threadIdx.x & 31;
   while (many) {
@@ -219,7 +205,7 @@ SA_DEV unsigned long long seq_work(const ChunkArgs& a, int b) {
     const int sn = __shfl_sync(0xffffffffu, N, src), sm = __shfl_sync(0xffffffffu, m, src);
     const int sp = __shfl_sync(0xffffffffu, pairs, src);
     unsigned long long x = 0;
-    for (int j = lane; j < sp; j += 32) x += pair_geom<BLK>(a, sn, sm, j).nb + kC0;
+    for (int j = lane; j < sp; j += 32) x += pair_geom(a, sn, sm, j).nb + kC0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lane == src) w = x;
@@ -249,13 +235,12 @@ SA_DEV unsigned long long scan64(unsigned long long v, unsigned long long* scrat
 }
 
 // This CTA's share of the work (every thread calls it; scratch: 18 words).
-template <int BLK>
 SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratch) {
   const int T = blockDim.x, tid = threadIdx.x, B = a.p.kv.B;
   const unsigned long long H = a.p.kv.Hkv;
   unsigned long long total = 0, w = 0, t, ex = 0;
   for (int base = 0; base < B; base += T) {
-    w = seq_work<BLK>(a, base + tid) * H;
+    w = seq_work(a, base + tid) * H;
     ex = scan64(w, scratch, t) + total;
     total += t;
   }
@@ -276,7 +261,7 @@ SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratc
   unsigned long long run = 0;
   for (int base = 0; base < B; base += T) {
     if (B > T) {
-      w = seq_work<BLK>(a, base + tid) * H;
+      w = seq_work(a, base + tid) * H;
       ex = scan64(w, scratch, t) + run;
       run += t;
     }
@@ -297,7 +282,7 @@ SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratc
     unsigned long long before = 0;
     for (int j0 = 0; j0 < pairs; j0 += 32) {
       const int j = j0 + tid;
-      const unsigned long long cst = j < pairs ? pair_geom<BLK>(a, N, m, j).nb + kC0 : 0;
+      const unsigned long long cst = j < pairs ? pair_geom(a, N, m, j).nb + kC0 : 0;
       unsigned long long x = cst;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -355,35 +340,10 @@ SA_DEV float max3(float a, float b, float c) {
   return r;
 }
 
-// 2^x of two finite values on the FMA pipe: x = n + f with n the nearest whole
-// number (by adding and subtracting 1.5 * 2^23) and |f| <= 1/2, 2^f by the
-// degree-4 polynomial of least relative error there (Remez exchange; 2.6e-6),
-// n added to its exponent.  The special-function unit gives 16 exponentials a
-// clock and SM, which by itself would take as long as both matrix products.
-SA_DEV unsigned long long poly_exp2(float x, float y) {
-  const unsigned long long magic = pack_f2(12582912.f, 12582912.f), nmagic = pack_f2(-12582912.f, -12582912.f);
-  const unsigned long long v = pack_f2(fmaxf(x, -126.f), fmaxf(y, -126.f));
-  const unsigned long long r = add_f2(v, magic);
-  const unsigned long long f = fma_f2(add_f2(r, nmagic), pack_f2(-1.f, -1.f), v);
-  unsigned long long p = fma_f2(pack_f2(9.570101911e-03f, 9.570101911e-03f), f, pack_f2(5.591786032e-02f, 5.591786032e-02f));
-  p = fma_f2(p, f, pack_f2(2.402474483e-01f, 2.402474483e-01f));
-  p = fma_f2(p, f, pack_f2(6.931218147e-01f, 6.931218147e-01f));
-  p = fma_f2(p, f, pack_f2(9.999992614e-01f, 9.999992614e-01f));
-  float r0, r1, p0, p1;
-  unpack_f2(r, r0, r1);
-  unpack_f2(p, p0, p1);
-  return pack_f2(__uint_as_float((__float_as_uint(r0) << 23) + __float_as_uint(p0)),
-                 __uint_as_float((__float_as_uint(r1) << 23) + __float_as_uint(p1)));
-}
-#ifndef SA_CHUNK_POLY
-#define SA_CHUNK_POLY 5
-#endif
-constexpr int kPoly = SA_CHUNK_POLY;  // of 16 pairs of exponentials, those taken by poly_exp2
-
 template <bool E4M3, int TERMS>
 __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using Sh = Shape<TERMS>;
-  constexpr int BLK = Sh::BLK, NS = Sh::NS;
+  constexpr int NS = Sh::NS, NB = Sh::NB;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Plan s_plan;
@@ -396,19 +356,18 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
   uint64_t* kv_empty = kv_full + NS;
   uint64_t* q_full = kv_empty + NS;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_empty + 1;   // [slot]
-  uint64_t* o_full = s_full + 2;    // [slot]
-  uint64_t* p_full = o_full + 2;    // [slot][part]
-  uint64_t* info_full = p_full + 2 * Sh::kParts;
+  uint64_t* s_full = q_empty + 1;   // [slot][buffer]
+  uint64_t* p_full = s_full + 4;    // [slot][buffer]
+  uint64_t* o_done = p_full + 4;    // [slot][parity of the PV]
+  uint64_t* info_full = o_done + 4;
   uint64_t* x_full = info_full + kInfo;
   uint64_t* x_empty = x_full + 1;
   uint64_t* drain = x_empty + 1;
-  uint64_t* raw_full = drain + 1;   // [2]
-  uint64_t* raw_empty = raw_full + 2;
+  uint64_t* raw_full = drain + 1;   // [NR]
+  uint64_t* raw_empty = raw_full + NR;
   volatile uint32_t* info = reinterpret_cast<uint32_t*>(base + Sh::off_info(E4M3));
-  volatile uint32_t* turn = info + kInfo;  // MMA groups issued so far
   unsigned char* raw = base + Sh::kOffRaw;
-  unsigned char* raw_scale = base + Sh::off_scale(E4M3);  // [2][BLK]
+  unsigned char* raw_scale = base + Sh::off_scale(E4M3);  // [NR][BLK]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float ninf = -__int_as_float(0x7f800000);
@@ -421,14 +380,15 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
-    *turn = 0u;
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(s_full + t, 1);
-      mbar_init(o_full + t, 1);
-      mbar_init(raw_full + t, 1);
-      mbar_init(raw_empty + t, 4);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(o_done + i, 1);
     }
-    for (int i = 0; i < 2 * Sh::kParts; ++i) mbar_init(p_full + i, 4);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(raw_full + i, 1);
+      mbar_init(raw_empty + i, 4);
+    }
     for (int i = 0; i < kInfo; ++i) mbar_init(info_full + i, 1);
     mbar_init(x_full, 4);
     mbar_init(x_empty, 4);
@@ -443,159 +403,142 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
     tc::tmem_relinquish();
   }
   grid_dep_wait();
-  make_plan<BLK>(a, &s_plan, s_scan);
+  make_plan(a, &s_plan, s_scan);
   if (tid == 0) a.recs[blockIdx.x] = ChunkRec{0, 0, 0, 0, 0};
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
   const PagedView& kv = a.p.kv;
-  Cursor<BLK> cur(a, s_plan);
+  Cursor cur(a, s_plan);
   Seg sg;
 
   if (warp >= 8 && warp < 12) {
     if (E4M3) reg_dealloc<56>();
     else reg_dealloc<72>();
-    if (warp == 8) {
-      // ---- producer
-      int n = 0, segs = 0, issued = 0;  // issued: K and V tiles
+    if (warp == 8 || warp == 11) {
+      // ---- producer of the K tiles (w = 0; of the queries, too) or the V tiles
+      const int w = warp == 11 ? 1 : 0;
+      const CUtensorMap* tmap = w ? &a.tmap_v : &a.tmap_k;
+      const uint8_t* scale = w ? kv.v_scale : kv.k_scale;
+      int n = 0, segs = 0;
       bool ok = true;
-      const int hb = a.hb, nbox = BLK / hb;
+      const int hb = a.hb, nbox = BLK / hb, sub = lane >> 1;  // this lane's box: rows sub * hb .., half lane & 1
       while (ok && cur.next(a, sg)) {
         if (sg.i0 == sg.i1) continue;
-        if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1u, status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+        if (w == 0) {
+          if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1u, status);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          const int tiles = sg.single ? 1 : 2;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * 2 * 128 * a.p.G * a.R));
+          __syncwarp();
+          if (lane < 2 * tiles)
+            tma_load_3d(qs + (lane >> 1) * kQTileBytes + (lane & 1) * (128 * 128), &a.tmap_q, 64 * (lane & 1),
+                        sg.g * a.p.G, sg.row0 + (lane >> 1) * a.R, q_full);
         }
-        const int tiles = sg.single ? 1 : 2;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * 2 * 128 * a.p.G * a.R));
-        __syncwarp();
-        if (lane < 2 * tiles)
-          tma_load_3d(qs + (lane >> 1) * kQTileBytes + (lane & 1) * (128 * 128), &a.tmap_q, 64 * (lane & 1),
-                      sg.g * a.p.G, sg.row0 + (lane >> 1) * a.R, q_full);
         ++segs;
+        // Table entry and slot of this lane's box of block i; entry -1 where no
+        // row of the pair needs it.  Looked up a block ahead: the lookup's
+        // latency would otherwise stand between a freed tile and its copy.
+        auto lookup = [&](int i, int& entry, int& slot) {
+          const int t0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK + sub * hb;
+          entry = -1;
+          slot = 0;
+          if (sub < nbox && i < sg.i1 && (t0 < sg.S || (t0 <= sg.p1 && t0 + hb > sg.lo))) {
+            const int p = t0 / kv.page_size;
+            slot = t0 - p * kv.page_size;
+            entry = __ldg(kv.table + (size_t)sg.b * kv.max_pages + p);
+            if (entry == -1) entry = -2;
+          }
+        };
+        int entry, slot;
+        lookup(sg.i0, entry, slot);
         for (int i = sg.i0; i < sg.i1; ++i, ++n) {
-          const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
-          // this lane's box: rows sub * hb .. of half (lane & 1)
-          const int sub = lane >> 1;
-          int page = -1, slot = 0;
-          uint32_t bad = 0;
-          if (sub < nbox) {
-            const int t0 = kb0 + sub * hb;
-            const bool need = t0 < sg.S || (t0 <= sg.p1 && t0 + hb > sg.lo);
-            if (need) {
-              const int p = t0 / kv.page_size;
-              slot = t0 - p * kv.page_size;
-              page = paged_page(kv, sg.b, p, status);
-              if (page < 0) bad = ((1u << (hb / 16)) - 1u) << (sub * (hb / 16));
-            }
+          int entry1, slot1;
+          lookup(i + 1, entry1, slot1);
+          const bool good = entry >= 0 && entry < kv.n_pages;
+          const int at = good ? entry : (int)kv.n_pages;  // past the pool: zeros
+          const uint32_t mine = !good && entry != -1 ? ((1u << (hb / 16)) - 1u) << (sub * (hb / 16)) : 0u;
+          const uint32_t bad = __reduce_or_sync(0xffffffffu, mine);
+          if (mine) flag_status(status, SA_ERR_DEVICE_CHECK);
+          const int x = 2 * n + w;
+          const int rs = E4M3 ? x % NR : x % NS;
+          const uint32_t use = (uint32_t)(E4M3 ? x / NR : x / NS);
+          if (use > 0) ok = mbar_wait((E4M3 ? raw_empty : kv_empty) + rs, (use - 1) & 1u, status);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
           }
-          bad = __reduce_or_sync(0xffffffffu, bad);
-          const int ks = (2 * n) % NS;
-          const uint32_t use = (uint32_t)((2 * n) / NS);
-          const int at = page < 0 ? (int)kv.n_pages : page;  // past the pool: zeros
-          if (E4M3) {
-            // codes of K, then of V, with their rows' scale bytes
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0 && !(lane & 1)));
-            for (int w = 0; w < 2; ++w) {
-              if (n > 0) ok = mbar_wait(raw_empty + w, (n - 1) & 1u, status);
-              if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-              }
-              if (w == 0 && lane == 0) {
-                info[n % kInfo] = bad;
-                mbar_arrive(info_full + n % kInfo);
-              }
-              if (lane == 0) mbar_arrive_expect_tx(raw_full + w, (uint32_t)Sh::kRaw + boxes * hb);
-              __syncwarp();
-              if (sub < nbox && !(lane & 1)) {
-                tma_load_4d(raw + w * Sh::kRaw + sub * hb * 128, w ? &a.tmap_v : &a.tmap_k, 0, slot, sg.g, at,
-                            raw_full + w);
-                if (page >= 0)
-                  bulk_load(raw_scale + w * BLK + sub * hb,
-                            (w ? kv.v_scale : kv.k_scale) + scale_index(kv, page, sg.g, slot), hb, raw_full + w);
-              }
-              issued = 2 * n + w + 1;
+          if (w == 0 && lane == 0) {
+            info[n % kInfo] = bad;
+            mbar_arrive(info_full + n % kInfo);
+          }
+          if (E4M3) {  // codes with their rows' scale bytes
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, good && !(lane & 1)));
+            if (lane == 0) mbar_arrive_expect_tx(raw_full + rs, (uint32_t)Sh::kRaw + boxes * hb);
+            __syncwarp();
+            if (sub < nbox && !(lane & 1)) {
+              tma_load_4d(raw + rs * Sh::kRaw + sub * hb * 128, tmap, 0, slot, sg.g, at, raw_full + rs);
+              if (good)
+                bulk_load(raw_scale + rs * BLK + sub * hb, scale + scale_index(kv, at, sg.g, slot), hb, raw_full + rs);
             }
-            if (!ok) break;
           } else {
-            for (int w = 0; w < 2; ++w) {
-              if (use > 0) ok = mbar_wait(kv_empty + ks + w, (use - 1) & 1u, status);
-              if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-              }
-              if (w == 0 && lane == 0) {
-                info[n % kInfo] = bad;
-                mbar_arrive(info_full + n % kInfo);
-              }
-              if (lane == 0) mbar_arrive_expect_tx(kv_full + ks + w, Sh::kSlot);
-              __syncwarp();
-              if (sub < nbox)
-                tma_load_4d(ring + (ks + w) * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128,
-                            w ? &a.tmap_v : &a.tmap_k, 64 * (lane & 1), slot, sg.g, at, kv_full + ks + w);
-              issued = 2 * n + w + 1;
-            }
-            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(kv_full + rs, Sh::kSlot);
+            __syncwarp();
+            if (sub < nbox)
+              tma_load_4d(ring + rs * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128, tmap, 64 * (lane & 1), slot,
+                          sg.g, at, kv_full + rs);
           }
+          entry = entry1;
+          slot = slot1;
         }
       }
       // every copy issued has landed before the CTA ends (bounded)
-      if (segs > 0) mbar_wait(q_full, (segs - 1) & 1u, nullptr);
-      if (E4M3) {
-        for (int x = max(0, issued - 2); x < issued; ++x) mbar_wait(raw_full + (x & 1), (x >> 1) & 1u, nullptr);
-      } else {
-        for (int x = max(0, issued - NS); x < issued; ++x) mbar_wait(kv_full + x % NS, (x / NS) & 1u, nullptr);
+      if (w == 0 && segs > 0) mbar_wait(q_full, (segs - 1) & 1u, nullptr);
+      constexpr int kRingBlocks = (E4M3 ? NR : NS) / 2;
+      for (int y = max(0, n - kRingBlocks); y < n; ++y) {
+        const int x = 2 * y + w;
+        if (E4M3) mbar_wait(raw_full + x % NR, (uint32_t)(x / NR) & 1u, nullptr);
+        else mbar_wait(kv_full + x % NS, (uint32_t)(x / NS) & 1u, nullptr);
       }
     } else if (warp < 11 && lane == 0) {
-      // ---- MMA issue of slot t.  Item k of a segment is block n0 + k of slot
-      // t (two tiles: every block, both slots in turn; one tile: every other
-      // block); its group is the PV of the slot's item before it and its QK.  A
-      // segment ends with the last items' PVs, a group each.  Groups are
-      // numbered over the whole CTA and issued in that order.
+      // ---- MMA issue of slot t: of two tiles, its tile and every block; of
+      // one tile, the blocks of its parity
       const int t = warp - 9;
       const uint32_t idesc_s = tc::idesc_f32acc(tc::kFmtBF16, 128, BLK);
       const uint32_t idesc_o = tc::idesc_f32acc(tc::kFmtBF16, 128, kHeadDim) | (1u << 16);  // V MN-major
       const uint32_t ts = tmem + kColS + 128u * t, to = tmem + kColO + 128u * t;
       const uint64_t k_desc = tc::smem_desc_sw128(ring), vt_desc = v_desc<Sh::kHalf>(ring);
       int n = 0, segs = 0;
-      uint32_t cnt = 0, order = 0;  // PVs issued by this slot; groups of both before the segment
+      uint32_t nqk = 0, npv = 0;   // QKs and PVs issued; at most NB apart
+      // the blocks whose PV is still to come, oldest first: ordinal, whether it
+      // is the segment's first, whether the other slot has no part in the block
+      int m0 = 0, m1 = 0;
+      bool first0 = false, first1 = false, twice0 = false, twice1 = false;
       bool ok = true;
-      // (a count, not a barrier: a slot may sit out any number of groups, and a
-      // barrier's parity tells only neighbouring phases apart)
-      auto my_turn = [&](uint32_t g) -> bool {
-        for (uint32_t i = 0; i < kSpinLimit; ++i)
-          if (*turn == g) return true;
-        flag_status(status, SA_ERR_TIMEOUT);
-        return false;
-      };
-      // P and V of block m have come
-      auto pv_ready = [&](int m) -> bool {
-        return mbar_wait(kv_full + (2 * m) % NS + 1, (uint32_t)((2 * m) / NS) & 1u, status) &&
-               mbar_wait(p_full + t * Sh::kParts, cnt & 1u, status);
-      };
-      auto pv = [&](int m, bool first, bool twice) -> bool {
-        const int vs = (2 * m) % NS + 1;
+      auto pv = [&]() -> bool {
+        const int vs = (2 * m0) % NS + 1;
+        const uint32_t b = npv % NB;
+        if (!mbar_wait(kv_full + vs, (uint32_t)((2 * m0) / NS) & 1u, status)) return false;
+        if (!mbar_wait(p_full + 2 * t + b, (npv / NB) & 1u, status)) return false;
+        tc::fence_after_sync();
         const uint64_t vd = vt_desc + (uint64_t)(vs * (Sh::kSlot >> 4));
-        constexpr int kSteps = BLK / 16 / Sh::kParts;
 #pragma unroll
-        for (int part = 0; part < Sh::kParts; ++part) {
-          if (part > 0) {
-            if (!mbar_wait(p_full + t * Sh::kParts + part, cnt & 1u, status)) return false;
-            tc::fence_after_sync();
-          }
+        for (int x = 0; x < TERMS; ++x)
 #pragma unroll
-          for (int x = 0; x < TERMS; ++x)
-#pragma unroll
-            for (int j = part * kSteps; j < (part + 1) * kSteps; ++j)
-              tc::mma_bf16_ts(to, ts + (uint32_t)(x * (BLK / 2) + 8 * j), vd + (uint64_t)(128 * j), idesc_o,
-                              !first || (x | j) != 0);
-        }
-        ++cnt;
+          for (int j = 0; j < BLK / 16; ++j)
+            tc::mma_bf16_ts(to, ts + 64u * b + (uint32_t)(x * (BLK / 2) + 8 * j), vd + (uint64_t)(128 * j), idesc_o,
+                            !first0 || (x | j) != 0);
+        tc::commit(o_done + 2 * t + (npv & 1u));
         tc::commit(kv_empty + vs);
-        if (twice) tc::commit(kv_empty + vs);  // the other slot has no part in this block
+        if (twice0) tc::commit(kv_empty + vs);
+        ++npv;
+        m0 = m1;
+        first0 = first1;
+        twice0 = twice1;
         return true;
       };
       while (ok && cur.next(a, sg)) {
@@ -603,46 +546,44 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         if (nblk == 0) continue;
         const bool single = sg.single;
         n += nblk;
-        if (!(ok = mbar_wait(q_full, segs & 1u, status))) break;
+        // the PVs of the segment before do not wait for these queries
+        while (ok && npv < nqk && !mbar_test(q_full, segs & 1u)) ok = pv();
+        if (!ok || !(ok = mbar_wait(q_full, segs & 1u, status))) break;
         ++segs;
         const int step = single ? 2 : 1;
-        const int k0 = single ? (n0 ^ t) & 1 : 0;  // this slot's first item
+        const int k0 = single ? (n0 ^ t) & 1 : 0;  // this slot's first block
         const uint64_t q_desc = tc::smem_desc_sw128(qs + (single ? 0 : t * kQTileBytes));
         if (k0 >= nblk) mbar_arrive(q_empty);
-        int k = k0;
-        for (; k < nblk; k += step) {
+        for (int k = k0; k < nblk; k += step) {
           const int m = n0 + k, ks = (2 * m) % NS;
           if (!(ok = mbar_wait(kv_full + ks, (uint32_t)((2 * m) / NS) & 1u, status))) break;
-          if (k > k0 && !(ok = pv_ready(m - step))) break;
-          if (!(ok = my_turn(order + (single ? k : 2 * k + t)))) break;
+          if (nqk - npv == NB && !(ok = pv())) break;  // its P is where this S goes
           tc::fence_after_sync();
-          if (k > k0 && !(ok = pv(m - step, k == k0 + step, single))) break;
           const uint64_t kd = k_desc + (uint64_t)(ks * (Sh::kSlot >> 4));
+          const uint32_t b = nqk % NB;
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              tc::mma_bf16_ss(ts, q_desc + (uint64_t)(c * (128 * 128 / 16) + 2 * x),
+              tc::mma_bf16_ss(ts + 64u * b, q_desc + (uint64_t)(c * (128 * 128 / 16) + 2 * x),
                               kd + (uint64_t)(c * (Sh::kHalf / 16) + 2 * x), idesc_s, (c | x) != 0);
-          *turn = *turn + 1u;
-          tc::commit(s_full + t);
+          tc::commit(s_full + 2 * t + b);
           tc::commit(kv_empty + ks);
           if (single) tc::commit(kv_empty + ks);
           if (k + step >= nblk) tc::commit(q_empty);
+          if (npv == nqk) {
+            m0 = m;
+            first0 = k == k0;
+            twice0 = single;
+          } else {
+            m1 = m;
+            first1 = k == k0;
+            twice1 = single;
+          }
+          ++nqk;
         }
-        if (!ok) break;
-        if (k > k0) {
-          const int last = k - step;  // this slot's last item
-          const uint32_t g = single ? (uint32_t)(nblk + (nblk >= 2 && last == nblk - 1 ? 1 : 0)) : (uint32_t)(2 * nblk + t);
-          if (!(ok = pv_ready(n0 + last))) break;
-          if (!(ok = my_turn(order + g))) break;
-          tc::fence_after_sync();
-          if (!(ok = pv(n0 + last, last == k0, single))) break;
-          *turn = *turn + 1u;
-          tc::commit(o_full + t);
-        }
-        order += (uint32_t)(single ? nblk + min(nblk, 2) : 2 * nblk + 2);
       }
+      while (ok && npv < nqk) ok = pv();
       // every MMA issued has completed before TMEM is freed (bounded)
       tc::commit(drain);
       mbar_wait(drain, 0, nullptr);
@@ -663,7 +604,8 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
           const uint32_t use = (uint32_t)((2 * n) / NS);
 #pragma unroll 1
           for (int w = 0; w < 2 && ok; ++w) {
-            ok = mbar_wait(raw_full + w, n & 1u, status);
+            const int rs = (2 * n + w) % NR;
+            ok = mbar_wait(raw_full + rs, (uint32_t)((2 * n + w) / NR) & 1u, status);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
               break;
@@ -672,8 +614,8 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
             uint32_t sc[BLK / 16];
 #pragma unroll
             for (int s = 0; s < BLK / 16; ++s) {
-              code[s] = lds128(raw + w * Sh::kRaw + (16 * s + r16) * 128 + 16 * c);
-              sc[s] = raw_scale[w * BLK + 16 * s + r16];
+              code[s] = lds128(raw + rs * Sh::kRaw + (16 * s + r16) * 128 + 16 * c);
+              sc[s] = raw_scale[rs * BLK + 16 * s + r16];
             }
             if (edge) {
 #pragma unroll
@@ -683,7 +625,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
               }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(raw_empty + w);
+            if (lane == 0) mbar_arrive(raw_empty + rs);
             if (use > 0) ok = mbar_wait(kv_empty + ks + w, (use - 1) & 1u, status);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
@@ -727,7 +669,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
     const int window = a.p.window, sinks = a.p.sinks;
     const float sl2 = a.scale_log2;
     int n = 0, nx = 0;
-    uint32_t cnt = 0, odone = 0;
+    uint32_t cnt = 0;  // blocks this slot has done
     bool ok = true;
     while (ok && cur.next(a, sg)) {
       const int row = (sg.single ? 0 : t * R) + rr;  // in the pair
@@ -740,7 +682,8 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
         ok = mbar_wait(info_full + n % kInfo, (uint32_t)(n / kInfo) & 1u, status);
         const uint32_t bad = info[n % kInfo];
-        ok = ok && mbar_wait(s_full + t, cnt & 1u, status);
+        const uint32_t b = cnt % NB, tb = ts + 64u * b;
+        ok = ok && mbar_wait(s_full + 2 * t + b, (cnt / NB) & 1u, status);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -750,7 +693,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         {
           uint32_t q[BLK / 32][32];
 #pragma unroll
-          for (int x = 0; x < BLK / 32; ++x) tc::ld_32x32b_x32(ts + 32 * x, q[x]);
+          for (int x = 0; x < BLK / 32; ++x) tc::ld_32x32b_x32(tb + 32 * x, q[x]);
           tc::wait_ld();
 #pragma unroll
           for (int x = 0; x < BLK / 32; ++x) {
@@ -785,8 +728,15 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         if (upd) mref = mn;
         lh *= alpha;
         if (used && __any_sync(0xffffffffu, upd)) {
-          // this slot's earlier PVs came before this block's QK in the issuing
-          // thread, so O is at rest here
+          // O is at rest once the slot's last PV is done (the next waits for P).
+          // Of one parity the PV barrier is never two phases past this wait:
+          // PV cnt + 1 needs the P that comes after it.
+          ok = mbar_wait(o_done + 2 * t + ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u, status);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t q[32];
@@ -825,23 +775,16 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         }
         unsigned long long rq[2] = {0ull, 0ull};  // partial sums, two values each
         const unsigned long long mul2 = pack_f2(mul, mul), nmn2 = pack_f2(nmn, nmn);
-        // P of 32 tokens; POLY: kPoly of 16 pairs on the FMA pipe (all finite)
-        auto exps = [&](auto poly, const int h2) {
+#pragma unroll
+        for (int h2 = 0; h2 < BLK / 32; ++h2) {  // P of 32 tokens
           uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float e0, e1;
             unpack_f2(fma_f2(pack_f2(sv[32 * h2 + 2 * j], sv[32 * h2 + 2 * j + 1]), mul2, nmn2), e0, e1);
-            unsigned long long e;
-            if (decltype(poly)::value && (j + 1) * kPoly / 16 != j * kPoly / 16) {
-              e = poly_exp2(e0, e1);
-              unpack_f2(e, e0, e1);
-            } else {
-              e0 = fast_exp2(e0);
-              e1 = fast_exp2(e1);
-              e = pack_f2(e0, e1);
-            }
-            rq[j & 1] = add_f2(rq[j & 1], e);
+            e0 = fast_exp2(e0);
+            e1 = fast_exp2(e1);
+            rq[j & 1] = add_f2(rq[j & 1], pack_f2(e0, e1));
             p1[j] = pack_bf16(e0, e1);
             if (TERMS == 3) {
               const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
@@ -849,27 +792,16 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
               p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
             }
           }
-          tc::st_32x32b_x16(ts + 16 * h2, p1);
+          tc::st_32x32b_x16(tb + 16 * h2, p1);
           if constexpr (TERMS == 3) {
-            tc::st_32x32b_x16(ts + 32 + 16 * h2, p2);
-            tc::st_32x32b_x16(ts + 64 + 16 * h2, p3);
+            tc::st_32x32b_x16(tb + 32 + 16 * h2, p2);
+            tc::st_32x32b_x16(tb + 64 + 16 * h2, p3);
           }
-        };
-#pragma unroll
-        for (int part = 0; part < Sh::kParts; ++part) {
-          constexpr int kPer = BLK / 32 / Sh::kParts;
-          if (TERMS == 1 && fast) {
-#pragma unroll
-            for (int h2 = part * kPer; h2 < (part + 1) * kPer; ++h2) exps(BoolTag<true>{}, h2);
-          } else {
-#pragma unroll
-            for (int h2 = part * kPer; h2 < (part + 1) * kPer; ++h2) exps(BoolTag<false>{}, h2);
-          }
-          tc::wait_st();
-          tc::fence_before_sync();  // P and the rescaled O before PV reads them
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + t * Sh::kParts + part);
         }
+        tc::wait_st();
+        tc::fence_before_sync();  // P and the rescaled O before PV reads them
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 2 * t + b);
         float s0, s1, s2, s3;
         unpack_f2(rq[0], s0, s1);
         unpack_f2(rq[1], s2, s3);
@@ -880,8 +812,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
       if (!ok) break;
       // ---- the row's result
       if (used) {
-        ok = mbar_wait(o_full + t, odone & 1u, status);
-        ++odone;
+        ok = mbar_wait(o_done + 2 * t + ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u, status);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -1066,7 +997,7 @@ cudaError_t launch(const ChunkArgs& a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-int chunk_block_tokens(bool fp32_out) { return fp32_out ? Shape<3>::BLK : Shape<1>::BLK; }
+int chunk_block_tokens() { return BLK; }
 
 cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st) {
   const bool f32 = a.p.out != nullptr;

@@ -81,7 +81,7 @@ struct ChunkArgs {
   ChunkRec* recs;                    // [grid]
 };
 cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st);
-int chunk_block_tokens(bool fp32_out);
+int chunk_block_tokens();
 // Opt a kernel into `bytes` of dynamic shared memory on the current device
 // (remembered per device; any thread may call it).
 cudaError_t allow_smem(const void* func, size_t bytes);
