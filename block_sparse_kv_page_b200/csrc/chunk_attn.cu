@@ -22,22 +22,31 @@
 // combine_kernel merges in CTA order: results do not depend on scheduling.
 //
 // CTA, warp-specialised, every wait bounded:
-//   warps 0-3 / 4-7  softmax of tile slot 0 / 1: thread = query vector (TMEM
-//                    lane), its whole row of BLK scores in registers;
-//   warps 8, 11      TMA of the queries and K tiles, of the V tiles (boxes of up to
+//   warps 0-7, 8-15  softmax of tile slot 0, 1: two threads per query vector
+//                    (TMEM lane), each half of the block's scores in registers.
+//                    Both use the row's reference maximum, which is only raised
+//                    when a score passes it by 2^8; whether any row needs that
+//                    is one barrier reduction over the pair of warps.  (With a
+//                    thread per row, two warps per scheduler, the chain of
+//                    loads, maxima and exponentials was bound by its latency:
+//                    2600 cycles per 64 tokens, 1024 of them exponentials.)
+//   warp 16          TMA of the queries and of the K and V tiles (boxes of up to
 //                    BLK rows inside a page; boxes that no row of the pair
 //                    needs, or whose page is bad, are fetched from past the
 //                    pool's end and so read as zeros);
-//   warps 9, 10      MMA issue of slot 0 / 1 (one thread each): S = Q K^T into
-//                    one of the slot's two S buffers and, once the softmax has
-//                    written P over S, O += P V.  The order of a slot is PV of
-//                    block n - 2, QK of block n, so the softmax always finds
-//                    the next scores ready and the products of one block run
-//                    under the softmax of the next.  (With one buffer of 128
-//                    tokens a slot's softmax and products alternate, and the
-//                    loop was bound by that chain's latency: 5080 cycles per
-//                    128 tokens and pair against 2240 of MMA time.)
-//   warps 12-15      (e4m3 cache) turn the codes of K and V, fetched into a
+//   warps 17, 18     issue S = Q K^T of slot 0 / 1 (one thread each) into one of
+//                    the slot's two S buffers;
+//   warp 19          issues O += P V of both slots once the softmax has written
+//                    P over S.  The softmax always finds the next scores ready,
+//                    and the products of one block run under the softmax of the
+//                    next.  (With one buffer of 128 tokens a slot's softmax and
+//                    products alternate and their latencies add up: 5080 cycles
+//                    per 128 tokens and pair against 2240 of MMA time.  The
+//                    products' operands fill shared memory's bandwidth, so a
+//                    wait on a barrier costs 200 cycles even when it is over;
+//                    one thread per slot for both products took 2490 cycles per
+//                    64 tokens, the three take about 1600.);
+//   warps 20-23      (e4m3 cache) turn the codes of K and V, fetched into a
 //                    ring of their own, into bf16 tiles: code * 2^k is exactly
 //                    a bf16, so the products are those of a bf16 cache of the
 //                    rounded values.
@@ -72,11 +81,12 @@ struct Shape {
   static constexpr int kOffRing = 2 * kQTileBytes;
   static constexpr int kRaw = BLK * 128;              // codes of a K or V tile
   static constexpr int kOffRaw = kOffRing + kRingBytes;   // e4m3 only: NR tiles of codes
-  static constexpr int kNumBars = 2 * NS + 2 + 2 * 6 + kInfo + 2 + 1 + 2 * NR;
+  static constexpr int kNumBars = 2 * NS + 2 + 2 * 6 + 2 + 1 + 2 * NR;
   static constexpr int off_bars(bool e4m3) { return kOffRaw + (e4m3 ? NR * kRaw : 0); }
   static constexpr int off_info(bool e4m3) { return off_bars(e4m3) + 8 * kNumBars; }
   static constexpr int off_scale(bool e4m3) { return (off_info(e4m3) + 4 * kInfo + 15) & ~15; }
-  static constexpr int smem(bool e4m3) { return 1024 + off_scale(e4m3) + (e4m3 ? NR * BLK : 0); }
+  static constexpr int off_x(bool e4m3) { return off_scale(e4m3) + (e4m3 ? NR * BLK : 0); }
+  static constexpr int smem(bool e4m3) { return 1024 + off_x(e4m3) + 2 * 128 * 4; }
 };
 
 template <int R>
@@ -87,6 +97,18 @@ template <int R>
 SA_DEV void reg_dealloc() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R));
 }
+
+// Whether `v` holds in any thread of the 2 warps that meet at barrier `id`.
+SA_DEV bool pair_any(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
+SA_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
 
 SA_DEV float fast_exp2(float x) {
   float y;
@@ -234,7 +256,7 @@ SA_DEV unsigned long long scan64(unsigned long long v, unsigned long long* scrat
   return base + x - v;
 }
 
-// This CTA's share of the work (every thread calls it; scratch: 18 words).
+// This CTA's share of the work (every thread calls it; scratch: 26 words).
 SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratch) {
   const int T = blockDim.x, tid = threadIdx.x, B = a.p.kv.B;
   const unsigned long long H = a.p.kv.Hkv;
@@ -267,13 +289,13 @@ SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratc
     }
     if (w && ex <= w0 && w0 < ex + w) {
       plan->b = base + tid;
-      scratch[16] = w0 - ex;
-      scratch[17] = w / H;
+      scratch[24] = w0 - ex;
+      scratch[25] = w / H;
     }
   }
   __syncthreads();
   if (tid < 32) {
-    const unsigned long long in = scratch[16], per = scratch[17];
+    const unsigned long long in = scratch[24], per = scratch[25];
     const int b = plan->b, g = (int)(in / per);
     const unsigned long long off = in - (unsigned long long)g * per;
     int r0;
@@ -341,13 +363,13 @@ SA_DEV float max3(float a, float b, float c) {
 }
 
 template <bool E4M3, int TERMS>
-__global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(E4M3 ? 768 : 640, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using Sh = Shape<TERMS>;
   constexpr int NS = Sh::NS, NB = Sh::NB;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Plan s_plan;
-  __shared__ unsigned long long s_scan[18];
+  __shared__ unsigned long long s_scan[26];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* qs = base;
@@ -359,8 +381,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
   uint64_t* s_full = q_empty + 1;   // [slot][buffer]
   uint64_t* p_full = s_full + 4;    // [slot][buffer]
   uint64_t* o_done = p_full + 4;    // [slot][parity of the PV]
-  uint64_t* info_full = o_done + 4;
-  uint64_t* x_full = info_full + kInfo;
+  uint64_t* x_full = o_done + 4;
   uint64_t* x_empty = x_full + 1;
   uint64_t* drain = x_empty + 1;
   uint64_t* raw_full = drain + 1;   // [NR]
@@ -368,6 +389,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
   volatile uint32_t* info = reinterpret_cast<uint32_t*>(base + Sh::off_info(E4M3));
   unsigned char* raw = base + Sh::kOffRaw;
   unsigned char* raw_scale = base + Sh::off_scale(E4M3);  // [NR][BLK]
+  volatile float* xchg = reinterpret_cast<float*>(base + Sh::off_x(E4M3));  // [slot][128]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float ninf = -__int_as_float(0x7f800000);
@@ -376,23 +398,22 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(kv_full + s, E4M3 ? 4 : 1);
-      mbar_init(kv_empty + s, 2);
+      mbar_init(kv_empty + s, s & 1 ? 1 : 2);  // K: both slots' issuers, V: one
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
+      mbar_init(p_full + i, 8);
       mbar_init(o_done + i, 1);
     }
     for (int i = 0; i < NR; ++i) {
       mbar_init(raw_full + i, 1);
       mbar_init(raw_empty + i, 4);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(info_full + i, 1);
-    mbar_init(x_full, 4);
-    mbar_init(x_empty, 4);
-    mbar_init(drain, 2);
+    mbar_init(x_full, 8);
+    mbar_init(x_empty, 8);
+    mbar_init(drain, 3);
     fence_barrier_init();
     prefetch_tmap(&a.tmap_q);
     prefetch_tmap(&a.tmap_k);
@@ -413,32 +434,27 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
   Cursor cur(a, s_plan);
   Seg sg;
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 16 && warp < 20) {
     if (E4M3) reg_dealloc<56>();
-    else reg_dealloc<72>();
-    if (warp == 8 || warp == 11) {
-      // ---- producer of the K tiles (w = 0; of the queries, too) or the V tiles
-      const int w = warp == 11 ? 1 : 0;
-      const CUtensorMap* tmap = w ? &a.tmap_v : &a.tmap_k;
-      const uint8_t* scale = w ? kv.v_scale : kv.k_scale;
-      int n = 0, segs = 0;
+    else reg_dealloc<64>();
+    if (warp == 16) {
+      // ---- producer
+      int n = 0, segs = 0, issued = 0;  // issued: K and V tiles
       bool ok = true;
       const int hb = a.hb, nbox = BLK / hb, sub = lane >> 1;  // this lane's box: rows sub * hb .., half lane & 1
       while (ok && cur.next(a, sg)) {
         if (sg.i0 == sg.i1) continue;
-        if (w == 0) {
-          if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1u, status);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          const int tiles = sg.single ? 1 : 2;
-          if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * 2 * 128 * a.p.G * a.R));
-          __syncwarp();
-          if (lane < 2 * tiles)
-            tma_load_3d(qs + (lane >> 1) * kQTileBytes + (lane & 1) * (128 * 128), &a.tmap_q, 64 * (lane & 1),
-                        sg.g * a.p.G, sg.row0 + (lane >> 1) * a.R, q_full);
+        if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1u, status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
         }
+        const int tiles = sg.single ? 1 : 2;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * 2 * 128 * a.p.G * a.R));
+        __syncwarp();
+        if (lane < 2 * tiles)
+          tma_load_3d(qs + (lane >> 1) * kQTileBytes + (lane & 1) * (128 * 128), &a.tmap_q, 64 * (lane & 1),
+                      sg.g * a.p.G, sg.row0 + (lane >> 1) * a.R, q_full);
         ++segs;
         // Table entry and slot of this lane's box of block i; entry -1 where no
         // row of the pair needs it.  Looked up a block ahead: the lookup's
@@ -456,7 +472,7 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         };
         int entry, slot;
         lookup(sg.i0, entry, slot);
-        for (int i = sg.i0; i < sg.i1; ++i, ++n) {
+        for (int i = sg.i0; ok && i < sg.i1; ++i, ++n) {
           int entry1, slot1;
           lookup(i + 1, entry1, slot1);
           const bool good = entry >= 0 && entry < kv.n_pages;
@@ -464,135 +480,138 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
           const uint32_t mine = !good && entry != -1 ? ((1u << (hb / 16)) - 1u) << (sub * (hb / 16)) : 0u;
           const uint32_t bad = __reduce_or_sync(0xffffffffu, mine);
           if (mine) flag_status(status, SA_ERR_DEVICE_CHECK);
-          const int x = 2 * n + w;
-          const int rs = E4M3 ? x % NR : x % NS;
-          const uint32_t use = (uint32_t)(E4M3 ? x / NR : x / NS);
-          if (use > 0) ok = mbar_wait((E4M3 ? raw_empty : kv_empty) + rs, (use - 1) & 1u, status);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          if (w == 0 && lane == 0) {
-            info[n % kInfo] = bad;
-            mbar_arrive(info_full + n % kInfo);
-          }
-          if (E4M3) {  // codes with their rows' scale bytes
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, good && !(lane & 1)));
-            if (lane == 0) mbar_arrive_expect_tx(raw_full + rs, (uint32_t)Sh::kRaw + boxes * hb);
-            __syncwarp();
-            if (sub < nbox && !(lane & 1)) {
-              tma_load_4d(raw + rs * Sh::kRaw + sub * hb * 128, tmap, 0, slot, sg.g, at, raw_full + rs);
-              if (good)
-                bulk_load(raw_scale + rs * BLK + sub * hb, scale + scale_index(kv, at, sg.g, slot), hb, raw_full + rs);
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, good && !(lane & 1)));
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            const CUtensorMap* tmap = w ? &a.tmap_v : &a.tmap_k;
+            const int x = 2 * n + w;
+            const int rs = E4M3 ? x % NR : x % NS;
+            const uint32_t use = (uint32_t)(E4M3 ? x / NR : x / NS);
+            if (use > 0) ok = mbar_wait((E4M3 ? raw_empty : kv_empty) + rs, (use - 1) & 1u, status);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
             }
-          } else {
-            if (lane == 0) mbar_arrive_expect_tx(kv_full + rs, Sh::kSlot);
-            __syncwarp();
-            if (sub < nbox)
-              tma_load_4d(ring + rs * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128, tmap, 64 * (lane & 1), slot,
-                          sg.g, at, kv_full + rs);
+            // the softmax reads it once the block's scores are there, which
+            // takes this K tile (ordered by the barriers on that way)
+            if (w == 0 && lane == 0) info[n % kInfo] = bad;
+            if (E4M3) {  // codes with their rows' scale bytes
+              if (lane == 0) mbar_arrive_expect_tx(raw_full + rs, (uint32_t)Sh::kRaw + boxes * hb);
+              __syncwarp();
+              if (sub < nbox && !(lane & 1)) {
+                tma_load_4d(raw + rs * Sh::kRaw + sub * hb * 128, tmap, 0, slot, sg.g, at, raw_full + rs);
+                if (good)
+                  bulk_load(raw_scale + rs * BLK + sub * hb,
+                            (w ? kv.v_scale : kv.k_scale) + scale_index(kv, at, sg.g, slot), hb, raw_full + rs);
+              }
+            } else {
+              if (lane == 0) mbar_arrive_expect_tx(kv_full + rs, Sh::kSlot);
+              __syncwarp();
+              if (sub < nbox)
+                tma_load_4d(ring + rs * Sh::kSlot + (lane & 1) * Sh::kHalf + sub * hb * 128, tmap, 64 * (lane & 1),
+                            slot, sg.g, at, kv_full + rs);
+            }
+            issued = x + 1;
           }
           entry = entry1;
           slot = slot1;
         }
       }
       // every copy issued has landed before the CTA ends (bounded)
-      if (w == 0 && segs > 0) mbar_wait(q_full, (segs - 1) & 1u, nullptr);
-      constexpr int kRingBlocks = (E4M3 ? NR : NS) / 2;
-      for (int y = max(0, n - kRingBlocks); y < n; ++y) {
-        const int x = 2 * y + w;
-        if (E4M3) mbar_wait(raw_full + x % NR, (uint32_t)(x / NR) & 1u, nullptr);
-        else mbar_wait(kv_full + x % NS, (uint32_t)(x / NS) & 1u, nullptr);
+      if (segs > 0) mbar_wait(q_full, (segs - 1) & 1u, nullptr);
+      if (E4M3) {
+        for (int x = max(0, issued - NR); x < issued; ++x) mbar_wait(raw_full + x % NR, (uint32_t)(x / NR) & 1u, nullptr);
+      } else {
+        for (int x = max(0, issued - NS); x < issued; ++x) mbar_wait(kv_full + x % NS, (uint32_t)(x / NS) & 1u, nullptr);
       }
-    } else if (warp < 11 && lane == 0) {
-      // ---- MMA issue of slot t: of two tiles, its tile and every block; of
-      // one tile, the blocks of its parity
-      const int t = warp - 9;
+    } else if (warp < 19 && lane == 0) {
+      // ---- QK of slot t: of two tiles, its tile and every block; of one tile,
+      // the blocks of its parity
+      const int t = warp - 17;
       const uint32_t idesc_s = tc::idesc_f32acc(tc::kFmtBF16, 128, BLK);
-      const uint32_t idesc_o = tc::idesc_f32acc(tc::kFmtBF16, 128, kHeadDim) | (1u << 16);  // V MN-major
-      const uint32_t ts = tmem + kColS + 128u * t, to = tmem + kColO + 128u * t;
-      const uint64_t k_desc = tc::smem_desc_sw128(ring), vt_desc = v_desc<Sh::kHalf>(ring);
+      const uint32_t ts = tmem + kColS + 128u * t;
+      const uint64_t k_desc = tc::smem_desc_sw128(ring);
       int n = 0, segs = 0;
-      uint32_t nqk = 0, npv = 0;   // QKs and PVs issued; at most NB apart
-      // the blocks whose PV is still to come, oldest first: ordinal, whether it
-      // is the segment's first, whether the other slot has no part in the block
-      int m0 = 0, m1 = 0;
-      bool first0 = false, first1 = false, twice0 = false, twice1 = false;
+      uint32_t c = 0;  // QKs issued
       bool ok = true;
-      auto pv = [&]() -> bool {
-        const int vs = (2 * m0) % NS + 1;
-        const uint32_t b = npv % NB;
-        if (!mbar_wait(kv_full + vs, (uint32_t)((2 * m0) / NS) & 1u, status)) return false;
-        if (!mbar_wait(p_full + 2 * t + b, (npv / NB) & 1u, status)) return false;
-        tc::fence_after_sync();
-        const uint64_t vd = vt_desc + (uint64_t)(vs * (Sh::kSlot >> 4));
-#pragma unroll
-        for (int x = 0; x < TERMS; ++x)
-#pragma unroll
-          for (int j = 0; j < BLK / 16; ++j)
-            tc::mma_bf16_ts(to, ts + 64u * b + (uint32_t)(x * (BLK / 2) + 8 * j), vd + (uint64_t)(128 * j), idesc_o,
-                            !first0 || (x | j) != 0);
-        tc::commit(o_done + 2 * t + (npv & 1u));
-        tc::commit(kv_empty + vs);
-        if (twice0) tc::commit(kv_empty + vs);
-        ++npv;
-        m0 = m1;
-        first0 = first1;
-        twice0 = twice1;
-        return true;
-      };
       while (ok && cur.next(a, sg)) {
-        const int nblk = sg.i1 - sg.i0, n0 = n;
-        if (nblk == 0) continue;
-        const bool single = sg.single;
-        n += nblk;
-        // the PVs of the segment before do not wait for these queries
-        while (ok && npv < nqk && !mbar_test(q_full, segs & 1u)) ok = pv();
-        if (!ok || !(ok = mbar_wait(q_full, segs & 1u, status))) break;
+        const int n0 = n;
+        if (sg.i1 == sg.i0) continue;
+        n += sg.i1 - sg.i0;
+        if (!(ok = mbar_wait(q_full, segs & 1u, status))) break;
         ++segs;
+        const bool single = sg.single;
         const int step = single ? 2 : 1;
-        const int k0 = single ? (n0 ^ t) & 1 : 0;  // this slot's first block
+        int m = single ? n0 + ((n0 ^ t) & 1) : n0;
         const uint64_t q_desc = tc::smem_desc_sw128(qs + (single ? 0 : t * kQTileBytes));
-        if (k0 >= nblk) mbar_arrive(q_empty);
-        for (int k = k0; k < nblk; k += step) {
-          const int m = n0 + k, ks = (2 * m) % NS;
+        if (m >= n) mbar_arrive(q_empty);
+#pragma unroll 1
+        for (; m < n; m += step) {
+          const int ks = (2 * m) % NS;
+          const uint32_t b = c % NB;
           if (!(ok = mbar_wait(kv_full + ks, (uint32_t)((2 * m) / NS) & 1u, status))) break;
-          if (nqk - npv == NB && !(ok = pv())) break;  // its P is where this S goes
+          // the buffer is free once the PV of the slot's block c - NB is done
+          if (c >= (uint32_t)NB && !(ok = mbar_wait(o_done + 2 * t + ((c - NB) & 1u), ((c - NB) >> 1) & 1u, status))) break;
           tc::fence_after_sync();
           const uint64_t kd = k_desc + (uint64_t)(ks * (Sh::kSlot >> 4));
-          const uint32_t b = nqk % NB;
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              tc::mma_bf16_ss(ts + 64u * b, q_desc + (uint64_t)(c * (128 * 128 / 16) + 2 * x),
-                              kd + (uint64_t)(c * (Sh::kHalf / 16) + 2 * x), idesc_s, (c | x) != 0);
+              tc::mma_bf16_ss(ts + 64u * b, q_desc + (uint64_t)(h * (128 * 128 / 16) + 2 * x),
+                              kd + (uint64_t)(h * (Sh::kHalf / 16) + 2 * x), idesc_s, (h | x) != 0);
           tc::commit(s_full + 2 * t + b);
           tc::commit(kv_empty + ks);
           if (single) tc::commit(kv_empty + ks);
-          if (k + step >= nblk) tc::commit(q_empty);
-          if (npv == nqk) {
-            m0 = m;
-            first0 = k == k0;
-            twice0 = single;
-          } else {
-            m1 = m;
-            first1 = k == k0;
-            twice1 = single;
-          }
-          ++nqk;
+          if (m + step >= n) tc::commit(q_empty);
+          ++c;
         }
       }
-      while (ok && npv < nqk) ok = pv();
       // every MMA issued has completed before TMEM is freed (bounded)
       tc::commit(drain);
       mbar_wait(drain, 0, nullptr);
+    } else if (warp == 19 && lane == 0) {
+      // ---- PV of both slots
+      const uint32_t idesc_o = tc::idesc_f32acc(tc::kFmtBF16, 128, kHeadDim) | (1u << 16);  // V MN-major
+      const uint64_t vt_desc = v_desc<Sh::kHalf>(ring);
+      int n = 0;
+      uint32_t c0 = 0, c1 = 0;  // PVs issued per slot
+      bool ok = true;
+      while (ok && cur.next(a, sg)) {
+        const int n0 = n, n_end = n + sg.i1 - sg.i0;
+        const bool single = sg.single;
+#pragma unroll 1
+        for (; ok && n < n_end; ++n) {
+          const int vs = (2 * n) % NS + 1;
+          if (!(ok = mbar_wait(kv_full + vs, (uint32_t)((2 * n) / NS) & 1u, status))) break;
+          const uint64_t vd = vt_desc + (uint64_t)(vs * (Sh::kSlot >> 4));
+#pragma unroll 1
+          for (int t = single ? (n & 1) : 0; t < (single ? (n & 1) + 1 : 2); ++t) {
+            const uint32_t c = t ? c1 : c0, b = c % NB;
+            if (!(ok = mbar_wait(p_full + 2 * t + b, (c / NB) & 1u, status))) break;
+            tc::fence_after_sync();
+            const bool acc = single ? n >= n0 + 2 : n > n0;
+#pragma unroll
+            for (int x = 0; x < TERMS; ++x)
+#pragma unroll
+              for (int j = 0; j < BLK / 16; ++j)
+                tc::mma_bf16_ts(tmem + kColO + 128u * t, tmem + kColS + 128u * t + 64u * b + (uint32_t)(x * (BLK / 2) + 8 * j),
+                                vd + (uint64_t)(128 * j), idesc_o, acc || (x | j) != 0);
+            tc::commit(o_done + 2 * t + (c & 1u));
+            if (t) ++c1;
+            else ++c0;
+          }
+          tc::commit(kv_empty + vs);
+        }
+      }
+      tc::commit(drain);
+      mbar_wait(drain, 0, nullptr);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 20) {
     // ---- e4m3 -> bf16: 8 threads per row, 16 rows at a time
     if constexpr (E4M3) {
-      reg_dealloc<88>();
-      const int x = tid - 384, c = x & 7, r16 = x >> 3;
+      reg_dealloc<72>();
+      const int x = tid - 640, c = x & 7, r16 = x >> 3;
       int n = 0;
       bool ok = true;
       while (ok && cur.next(a, sg)) {
@@ -655,148 +674,137 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         }
       }
     }
-  } else if (warp < 8) {
-    // ---- softmax of slot t
-    if (E4M3) reg_alloc<184>();
-    else reg_alloc<216>();
-    const int t = warp >> 2, quarter = warp & 3;
+  } else {
+    // ---- softmax of slot t, columns 32 half .. 32 half + 31 of a block
+    if (E4M3) reg_alloc<88>();
+    else reg_alloc<104>();
+    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int id = 1 + 4 * t + quarter;  // barrier of the two warps that share rows
     const int r = 32 * quarter + lane;
     const int G = a.p.G, R = a.R;
     const int rr = r / G, hh = r - rr * G;
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     const uint32_t ts = tmem + lane_off + kColS + 128u * t;
-    const uint32_t to = tmem + lane_off + kColO + 128u * t;
+    const uint32_t to = tmem + lane_off + kColO + 128u * t + 64u * half;  // this thread's half of the dims
     const int window = a.p.window, sinks = a.p.sinks;
     const float sl2 = a.scale_log2;
+    volatile float* xr = xchg + 128 * t + r;
     int n = 0, nx = 0;
     uint32_t cnt = 0;  // blocks this slot has done
-    bool ok = true;
-    while (ok && cur.next(a, sg)) {
+    // After a wait has run out the warp goes through the same steps without
+    // waiting, so that its partner never stands at their barrier alone.
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+    };
+    while (cur.next(a, sg)) {
       const int row = (sg.single ? 0 : t * R) + rr;  // in the pair
       const bool vok = r < G * R && row < sg.rows;
       const int qpos = vok ? sg.p0 + row : -1;
-      float mref = ninf, lh = 0.f;  // reference maximum (log2 units), sum against it
+      float mref = ninf, lh = 0.f;  // reference maximum (log2 units); this half's sum against it
       bool used = false;
       for (int i = sg.i0; i < sg.i1; ++i, ++n) {
         if (sg.single && (n & 1) != t) continue;
         const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
-        ok = mbar_wait(info_full + n % kInfo, (uint32_t)(n / kInfo) & 1u, status);
-        const uint32_t bad = info[n % kInfo];
+        const int kh0 = kb0 + 32 * half;  // this thread's first token
         const uint32_t b = cnt % NB, tb = ts + 64u * b;
-        ok = ok && mbar_wait(s_full + 2 * t + b, (cnt / NB) & 1u, status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        wait(s_full + 2 * t + b, (cnt / NB) & 1u);
         tc::fence_after_sync();
-        float sv[BLK];
-        {
-          uint32_t q[BLK / 32][32];
+        uint32_t q[32];
+        tc::ld_32x32b_x32(tb + 32 * half, q);
+        const uint32_t bad = info[n % kInfo];
+        tc::wait_ld();
+        tc::reg_fence(q);
+        float sv[32];
 #pragma unroll
-          for (int x = 0; x < BLK / 32; ++x) tc::ld_32x32b_x32(tb + 32 * x, q[x]);
-          tc::wait_ld();
-#pragma unroll
-          for (int x = 0; x < BLK / 32; ++x) {
-            tc::reg_fence(q[x]);
-#pragma unroll
-            for (int y = 0; y < 32; ++y) sv[32 * x + y] = __uint_as_float(q[x][y]);
-          }
-        }
-        // Blocks that every row of the warp sees whole skip the masks, and with
-        // a positive scale the maximum is taken on raw scores.
-        const bool whole = kb0 + BLK - 1 <= qpos && (window == 0 || kb0 > qpos - window || kb0 + BLK <= sinks);
-        const bool fast = bad == 0 && sl2 > 0.f && __all_sync(0xffffffffu, !vok || whole);
-        float mq[4] = {ninf, ninf, ninf, ninf}, mul = sl2;
+        for (int x = 0; x < 32; ++x) sv[x] = __uint_as_float(q[x]);
+        // Halves of blocks that every row of the warp sees whole skip the masks,
+        // and with a positive scale the maximum is taken on raw scores.
+        const bool all = kh0 + 31 <= qpos && (window == 0 || kh0 > qpos - window || kh0 + 32 <= sinks);
+        const bool fast = bad == 0 && sl2 > 0.f && __all_sync(0xffffffffu, !vok || all);
+        float mq[2] = {ninf, ninf}, mul = sl2;
         if (fast) {
 #pragma unroll
-          for (int x = 0; x < BLK; x += 2) mq[(x >> 1) & 3] = max3(mq[(x >> 1) & 3], sv[x], sv[x + 1]);
+          for (int x = 0; x < 32; x += 2) mq[(x >> 1) & 1] = max3(mq[(x >> 1) & 1], sv[x], sv[x + 1]);
         } else {
           mul = 1.f;
 #pragma unroll
-          for (int x = 0; x < BLK; ++x) {
-            const int tok = kb0 + x;
-            const bool see = row_sees(qpos, tok, window, sinks) && !((bad >> (x / 16)) & 1u);
+          for (int x = 0; x < 32; ++x) {
+            const bool see = row_sees(qpos, kh0 + x, window, sinks) && !((bad >> (2 * half + x / 16)) & 1u);
             sv[x] = see ? sv[x] * sl2 : ninf;
-            mq[x & 3] = fmaxf(mq[x & 3], sv[x]);
+            mq[x & 1] = fmaxf(mq[x & 1], sv[x]);
           }
         }
-        float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        float mx = fmaxf(mq[0], mq[1]);
         if (fast) mx *= sl2;
-        const float mn = fmaxf(mref, mx);
-        const bool upd = mn != ninf && (mref == ninf || mn > mref + 8.f);
-        const float alpha = !upd ? 1.f : (mref == ninf ? 0.f : fast_exp2(mref - mn));
-        if (upd) mref = mn;
-        lh *= alpha;
-        if (used && __any_sync(0xffffffffu, upd)) {
-          // O is at rest once the slot's last PV is done (the next waits for P).
-          // Of one parity the PV barrier is never two phases past this wait:
-          // PV cnt + 1 needs the P that comes after it.
-          ok = mbar_wait(o_done + 2 * t + ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u, status);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
+        if (pair_any(id, mx > mref + 8.f || (mref == ninf && mx > ninf))) {
+          // rare: the row's maximum over both halves, and what follows from it
+          if (half == 0) *xr = mx;
+          pair_sync(id);
+          if (half == 1) {
+            mx = fmaxf(mx, *xr);
+            *xr = mx;
           }
-          tc::fence_after_sync();
+          pair_sync(id);
+          if (half == 0) mx = *xr;
+          const bool upd = mx > mref + 8.f || (mref == ninf && mx > ninf);
+          const float alpha = !upd ? 1.f : (mref == ninf ? 0.f : fast_exp2(mref - mx));
+          if (upd) mref = mx;
+          lh *= alpha;
+          if (used && __any_sync(0xffffffffu, upd)) {
+            // O is at rest once the slot's last PV is done (the next waits for
+            // P).  Of one parity the PV barrier is never two phases past this
+            // wait: PV cnt + 1 needs the P that comes after it.
+            wait(o_done + 2 * t + ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u);
+            tc::fence_after_sync();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t q[32];
-            tc::ld_32x32b_x32(to + 32 * c, q);
-            tc::wait_ld();
-            tc::reg_fence(q);
-            uint32_t lo[16], hi[16];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[16];
+              tc::ld_32x32b_x16(to + 16 * c, o);
+              tc::wait_ld();
+              tc::reg_fence(o);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              lo[x] = __float_as_uint(__uint_as_float(q[x]) * alpha);
-              hi[x] = __float_as_uint(__uint_as_float(q[16 + x]) * alpha);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tc::st_32x32b_x16(to + 16 * c, o);
             }
-            tc::st_32x32b_x16(to + 32 * c, lo);
-            tc::st_32x32b_x16(to + 32 * c + 16, hi);
           }
         }
         const float nmn = mref == ninf ? 0.f : -mref;  // nothing seen so far: every p is exp2(-inf) = 0
+        unsigned long long rq[2] = {0ull, 0ull};  // partial sums, two values each
+        const unsigned long long mul2 = pack_f2(mul, mul), nmn2 = pack_f2(nmn, nmn);
+        uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float e0, e1;
+          unpack_f2(fma_f2(pack_f2(sv[2 * j], sv[2 * j + 1]), mul2, nmn2), e0, e1);
+          e0 = fast_exp2(e0);
+          e1 = fast_exp2(e1);
+          rq[j & 1] = add_f2(rq[j & 1], pack_f2(e0, e1));
+          p1[j] = pack_bf16(e0, e1);
+          if (TERMS == 3) {
+            const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
+            p2[j] = pack_bf16(d0, d1);
+            p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
+          }
+        }
+        // P lies over S: the other half's scores have been read (pair_any)
+        tc::st_32x32b_x16(tb + 16 * half, p1);
+        if constexpr (TERMS == 3) {
+          tc::st_32x32b_x16(tb + 32 + 16 * half, p2);
+          tc::st_32x32b_x16(tb + 64 + 16 * half, p3);
+        }
         // bf16 tiles hold whatever the cache has at tokens that no row of the
         // pair sees: their V rows are zeroed before PV reads them
         if (!E4M3 && (kb0 + BLK > sg.p1 + 1 || (kb0 < sg.lo && kb0 + BLK > sg.S))) {
           const int vs = (2 * n) % NS + 1;
-          ok = mbar_wait(kv_full + vs, (uint32_t)((2 * n) / NS) & 1u, status);
+          wait(kv_full + vs, (uint32_t)((2 * n) / NS) & 1u);
           unsigned char* vt = ring + vs * Sh::kSlot;
-          if (ok) {
-            for (int x = r; x < BLK * 16; x += 128) {
-              const int y = x >> 4, ch = x & 15, tok = kb0 + y;
-              if (!(tok < sg.S || (tok >= sg.lo && tok <= sg.p1)))
-                *reinterpret_cast<uint4*>(vt + (ch >> 3) * Sh::kHalf + swz128(y, ch & 7)) = make_uint4(0u, 0u, 0u, 0u);
-            }
+          for (int x = 128 * half + r; x < BLK * 16; x += 256) {
+            const int y = x >> 4, ch = x & 15, tok = kb0 + y;
+            if (!(tok < sg.S || (tok >= sg.lo && tok <= sg.p1)))
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * Sh::kHalf + swz128(y, ch & 7)) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async();
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-        }
-        unsigned long long rq[2] = {0ull, 0ull};  // partial sums, two values each
-        const unsigned long long mul2 = pack_f2(mul, mul), nmn2 = pack_f2(nmn, nmn);
-#pragma unroll
-        for (int h2 = 0; h2 < BLK / 32; ++h2) {  // P of 32 tokens
-          uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float e0, e1;
-            unpack_f2(fma_f2(pack_f2(sv[32 * h2 + 2 * j], sv[32 * h2 + 2 * j + 1]), mul2, nmn2), e0, e1);
-            e0 = fast_exp2(e0);
-            e1 = fast_exp2(e1);
-            rq[j & 1] = add_f2(rq[j & 1], pack_f2(e0, e1));
-            p1[j] = pack_bf16(e0, e1);
-            if (TERMS == 3) {
-              const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
-              p2[j] = pack_bf16(d0, d1);
-              p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
-            }
-          }
-          tc::st_32x32b_x16(tb + 16 * h2, p1);
-          if constexpr (TERMS == 3) {
-            tc::st_32x32b_x16(tb + 32 + 16 * h2, p2);
-            tc::st_32x32b_x16(tb + 64 + 16 * h2, p3);
-          }
         }
         tc::wait_st();
         tc::fence_before_sync();  // P and the rescaled O before PV reads them
@@ -809,55 +817,53 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         ++cnt;
         used = true;
       }
-      if (!ok) break;
-      // ---- the row's result
-      if (used) {
-        ok = mbar_wait(o_done + 2 * t + ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u, status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+      // ---- the row's result: this thread's half of the dims; first the sum of
+      // both halves of the tokens
+      if (sg.nb > 0) {
+        if (half == 0) *xr = lh;
+        pair_sync(id);
+        if (half == 1) {
+          lh = *xr + lh;
+          *xr = lh;
         }
+        pair_sync(id);
+        if (half == 0) lh = *xr;
+      }
+      if (used) {
+        wait(o_done + 2 * t + ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u);
         tc::fence_after_sync();
       }
       const bool whole = sg.i0 == 0 && sg.i1 == sg.nb;
-      float f0 = 1.f, f1 = 0.f;              // weights of this slot's and the other slot's result
+      const bool merge = sg.single && sg.nb > 0;  // both slots have a part of the rows
+      float f0 = 1.f, f1 = 0.f;                   // weights of this slot's and the other slot's result
       const float* other = nullptr;
       float* xrow = a.xbuf + ((size_t)blockIdx.x * 128 + r) * kChunkPart;
-      if (sg.single && sg.nb > 0) {
-        if (t == 1) {
-          if (nx > 0) ok = mbar_wait(x_empty, (nx - 1) & 1u, status);
-        } else {
-          ok = mbar_wait(x_full, nx & 1u, status);
+      if (merge && t == 1 && nx > 0) wait(x_empty, (nx - 1) & 1u);
+      if (merge && t == 0) {
+        wait(x_full, nx & 1u);
+        const float m1 = __ldcg(xrow + kHeadDim), l1 = __ldcg(xrow + kHeadDim + 1);
+        const float M = fmaxf(mref, m1);
+        if (M != ninf) {
+          f0 = fast_exp2(mref - M);
+          f1 = fast_exp2(m1 - M);
         }
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        if (t == 0) {
-          const float m1 = __ldcg(xrow + kHeadDim), l1 = __ldcg(xrow + kHeadDim + 1);
-          const float M = fmaxf(mref, m1);
-          if (M != ninf) {
-            f0 = fast_exp2(mref - M);
-            f1 = fast_exp2(m1 - M);
-          }
-          lh = lh * f0 + l1 * f1;
-          mref = M;
-          other = xrow;
-        }
+        lh = lh * f0 + l1 * f1;
+        mref = M;
+        other = xrow;
       }
       float* part = nullptr;  // where an unnormalised result goes
-      if (sg.single && sg.nb > 0 && t == 1) {
+      if (merge && t == 1) {
         part = xrow;
       } else if (!whole) {
         part = a.parts + ((((size_t)blockIdx.x * 2 + (sg.i0 == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart;
       }
       const float inv = part ? 1.f : (lh > 0.f ? 1.f / lh : 0.f);
       const size_t orow = vok ? (size_t)(sg.row0 + row) * a.p.Hq + (size_t)sg.g * G + hh : 0;
-      const bool skip = sg.single && t == 1 && sg.nb == 0;  // slot 0 writes the zeros
+      const bool mine = vok && !dead && !(sg.single && t == 1 && sg.nb == 0);  // (then slot 0 writes the zeros)
       f0 *= inv;
       f1 *= inv;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t q[16];
         if (used) {
           tc::ld_32x32b_x16(to + 16 * c, q);
@@ -870,36 +876,37 @@ __global__ void __launch_bounds__(E4M3 ? 512 : 384, 1) chunk_kernel(const __grid
         float o[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) o[x] = __uint_as_float(q[x]) * f0;
+        const int d0 = 64 * half + 16 * c;
         if (other) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(other + 16 * c + x));
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(other + d0 + x));
             o[x] += y.x * f1;
             o[x + 1] += y.y * f1;
             o[x + 2] += y.z * f1;
             o[x + 3] += y.w * f1;
           }
         }
-        if (vok && !skip) {
+        if (mine) {
           if (part || a.p.out) {
-            float* d = (part ? part : a.p.out + orow * kHeadDim) + 16 * c;
+            float* d = (part ? part : a.p.out + orow * kHeadDim) + d0;
 #pragma unroll
             for (int x = 0; x < 16; x += 4)
               *reinterpret_cast<float4*>(d + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
           } else {
-            uint4* d = reinterpret_cast<uint4*>(a.p.out_bf16 + orow * kHeadDim + 16 * c);
+            uint4* d = reinterpret_cast<uint4*>(a.p.out_bf16 + orow * kHeadDim + d0);
             d[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
             d[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]), pack_bf16(o[12], o[13]),
                               pack_bf16(o[14], o[15]));
           }
         }
       }
-      if (vok && !skip) {
+      if (mine && half == 0) {
         if (part) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mref, lh);
         else if (a.p.lse) a.p.lse[orow] = lh > 0.f ? mref * kLn2 + logf(lh) : ninf;
         if (sg.i0 == 0 && qpos < 0) flag_status(status, SA_ERR_DEVICE_CHECK);
       }
-      if (sg.single && sg.nb > 0) {
+      if (merge) {
         __threadfence_block();
         __syncwarp();
         if (lane == 0) mbar_arrive(t == 1 ? x_full : x_empty);
@@ -992,7 +999,7 @@ cudaError_t launch(const ChunkArgs& a, int grid, cudaStream_t st) {
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const cudaError_t e = allow_smem((const void*)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, (unsigned)grid, E4M3 ? 512 : 384, smem, st, a);
+  return launch_pdl(k, (unsigned)grid, E4M3 ? 768 : 640, smem, st, a);
 }
 
 }  // namespace
