@@ -1,5 +1,5 @@
 // C-ABI entry points of the paged cache: host-side argument validation and
-// kernel launches (cache_io.cu, paged_attn.cu).
+// kernel launches (cache_io.cu, chunk_attn.cu, paged_decode.cu).
 //
 // Workspace: the layout of the other calls (api.cu): the status word at 0, the
 // unit counters (not used here, left as they are), per-call scratch from
@@ -55,6 +55,7 @@ PagedScratch paged_scratch() {
   s.xbuf = s.parts + align256(sms * 2 * 2 * 128 * kChunkPart * sizeof(float));
   s.recs = s.xbuf + align256(sms * 128 * kChunkPart * sizeof(float));
   s.total = s.recs + align256(sms * sizeof(ChunkRec));
+  // (the decode's parts and records, smaller, lie in the same place)
   return s;
 }
 
@@ -132,6 +133,34 @@ sa_status check_heads(const sa_paged_desc* kv, int n_q_heads, int* G) {
   return SA_OK;
 }
 
+// Tensor maps of the pool, [n_pages][Hkv][page_size][128], boxes of `rows` rows
+// of 128 bytes (64 bf16 or 128 codes).
+bool cache_maps(const PagedView& kv, CUtensorMap* k, CUtensorMap* v, int rows, bool swizzle) {
+  const unsigned long long d[4] = {kHeadDim, (unsigned long long)kv.page_size, (unsigned long long)kv.Hkv,
+                                   (unsigned long long)kv.n_pages};
+  const unsigned long long s[3] = {(unsigned long long)kv.token_stride, (unsigned long long)kv.head_stride,
+                                   (unsigned long long)kv.page_stride};
+  const unsigned b[4] = {kv.e4m3 ? 128u : 64u, (unsigned)rows, 1, 1};
+  const CUtensorMapDataType dt = kv.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return encode_tmap_nd(k, kv.k, dt, 4, d, s, b, swizzle) && encode_tmap_nd(v, kv.v, dt, 4, d, s, b, swizzle);
+}
+
+sa_status decode(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
+  PagedDecodeArgs a{};
+  const PagedView& kv = p.kv;
+  a.p = p;
+  a.scale_log2 = p.scale * kLog2e;
+  if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, 16, true)) return SA_ERR_CUDA;
+  const int grid = paged_decode_grid(device_sm_count());
+  const long long units = (long long)kv.B * kv.Hkv;
+  a.by_unit = units <= grid ? 1 : 0;
+  const size_t part_bytes = align256((size_t)grid * paged_decode_part_floats() * sizeof(float));
+  a.parts = (float*)(ws + kScratch);
+  a.recs = (int4*)(ws + kScratch + part_bytes);
+  if (kScratch + part_bytes + (size_t)grid * sizeof(int4) > paged_scratch().total) return SA_ERR_WORKSPACE;
+  return launched(launch_paged_decode(a, grid, a.by_unit ? (int)units : grid, st));
+}
+
 sa_status chunk(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   ChunkArgs a{};
   const PagedView& kv = p.kv;
@@ -144,16 +173,8 @@ sa_status chunk(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   const unsigned long long qs[2] = {kHeadDim * 2, (unsigned long long)p.q_row_stride * 2};
   const unsigned qb[3] = {64, (unsigned)p.G, (unsigned)a.R};
   if (!encode_tmap_nd(&a.tmap_q, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, qd, qs, qb, true)) return SA_ERR_CUDA;
-  const unsigned long long d[4] = {kHeadDim, (unsigned long long)kv.page_size, (unsigned long long)kv.Hkv,
-                                   (unsigned long long)kv.n_pages};
-  const unsigned long long s[3] = {(unsigned long long)kv.token_stride, (unsigned long long)kv.head_stride,
-                                   (unsigned long long)kv.page_stride};
   // bf16: halves of 64 dims, swizzled for the MMA; e4m3: whole rows of codes
-  const unsigned b[4] = {kv.e4m3 ? 128u : 64u, (unsigned)a.hb, 1, 1};
-  const CUtensorMapDataType dt = kv.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!encode_tmap_nd(&a.tmap_k, kv.k, dt, 4, d, s, b, !kv.e4m3) ||
-      !encode_tmap_nd(&a.tmap_v, kv.v, dt, 4, d, s, b, !kv.e4m3))
-    return SA_ERR_CUDA;
+  if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, a.hb, !kv.e4m3)) return SA_ERR_CUDA;
   const PagedScratch sc = paged_scratch();
   a.parts = (float*)(ws + sc.parts);
   a.xbuf = (float*)(ws + sc.xbuf);
@@ -191,7 +212,7 @@ sa_status paged_attention(const sa_paged_desc* kv, const void* q, int64_t q_row_
   a.status = (int*)ws;
   // a window that no position passes is none (and keeps p - window in range)
   if ((long long)window > (long long)kv->max_pages * kv->page_size) a.window = 0;
-  if (!row_off) return launched(launch_paged_attn(a, (cudaStream_t)stream));
+  if (!row_off) return decode(a, (unsigned char*)ws, (cudaStream_t)stream);
   return chunk(a, (unsigned char*)ws, (cudaStream_t)stream);
 }
 

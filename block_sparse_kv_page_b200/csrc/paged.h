@@ -61,7 +61,6 @@ struct PagedAttnArgs {
   float* lse;                  // nullable
   int* status;
 };
-cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t st);
 
 // Chunk attention (chunk_attn.cu).
 constexpr int kChunkPart = 128 + 4;  // floats of a partial result: acc[128], reference maximum, sum, 2 unused
@@ -82,6 +81,19 @@ struct ChunkArgs {
 };
 cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st);
 int chunk_block_tokens();
+// Single-token attention (paged_decode.cu).
+struct PagedDecodeArgs {
+  CUtensorMap tmap_k, tmap_v;        // [n_pages][Hkv][page_size][128], box 1 x 1 x 16 x 128 bytes, 128B swizzle
+  PagedAttnArgs p;                   // row b of sequence b
+  float scale_log2;                  // scale * log2(e)
+  int by_unit;                       // recs by unit (b * Hkv + g) instead of by CTA
+  float* parts;                      // [grid][head, tail segment][8 heads][132]
+  int4* recs;                        // cut units: first CTA (-1: none), last CTA, b, g
+};
+int paged_decode_grid(int sms);
+size_t paged_decode_part_floats();   // per CTA
+// recs: entries of a.recs, the smaller of units and grid
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int grid, int recs, cudaStream_t st);
 // Opt a kernel into `bytes` of dynamic shared memory on the current device
 // (remembered per device; any thread may call it).
 cudaError_t allow_smem(const void* func, size_t bytes);

@@ -1,0 +1,591 @@
+// Single-token attention over the paged cache: one row per sequence.
+//
+// Mathematics: the newest row of sequence b, position N - 1, query head h of KV
+// head g: out = sum exp(z_t - lse) v_t over the visible tokens, z_t = scale
+// q . k_t, in one pass with a running maximum and sum.  Every visible token's K
+// and V are read once for the G <= 8 heads that share them; that read bounds it.
+//
+// Units are (sequence, KV head) pairs, cut into tiles of 16 tokens (those of
+// the first tokens and of the window; a page is whole tiles).  The work is the
+// list of all units' tiles; the grid takes equal runs of it (each unit counting
+// kC0 tiles more, the cost of starting one), cut anywhere, so that one long
+// sequence fills every SM and ragged batches stay balanced.  The prefix is
+// computed from the lengths on the device by every CTA.  A unit cut between
+// CTAs leaves unnormalised parts in the workspace, merged by combine_kernel in
+// CTA order: results do not depend on scheduling.
+//
+// Inside a CTA the four warps take tiles in turn, each with a ring of its own:
+// TMA boxes of 16 rows, 128B-swizzled, three CTAs and 192 KiB of rings per SM.
+// Per tile (tensor cores, fp32 accumulation):
+//   S^T [16 tokens x 8 heads] = K Q^T;
+//   P: exp2 of the scaled scores in fp32, as two bf16 terms (three for fp32
+//      outputs: 2^-17 and 2^-25 of a weight), moved to the B layout;
+//   O^T [128 dims x 8 heads] += V^T P^T.
+// e4m3: codes become bf16 fragments in registers.  The order of the reduction
+// axis is free as long as both operands share it, so a lane takes whole 16-byte
+// pieces of a row: 32 dims of two tokens for K, 16 dims of four tokens for V,
+// free of bank conflicts under the swizzle.  The rows' scales (powers of two)
+// multiply the scores and the weights, 4 values a lane instead of 256.
+#include "paged.cuh"
+#include "internal.h"
+
+namespace sa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kC0 = 6;          // cost of starting a unit, in tiles
+constexpr int kMinShare = 24;   // least work of a CTA
+constexpr int kPart = kHeadDim + 4;          // floats of a head's part: acc, maximum, sum, 2 unused
+constexpr int kMergeBytes = kWarps * kMaxGroup * (kHeadDim + 2) * 4;
+
+template <bool E4M3>
+struct Ring {
+  static constexpr int kBox = 2048;                  // 16 rows x 128 B
+  static constexpr int kTile = (E4M3 ? 2 : 4) * kBox;
+  static constexpr int kStages = E4M3 ? 4 : 2;
+  static constexpr int kRing = kWarps * kStages * kTile;
+  static constexpr int kOffScale = kRing;            // [warp][stage][K 16 | V 16]
+  static constexpr int kOffBars = kOffScale + (E4M3 ? kWarps * kStages * 32 : 0);
+  static constexpr int kSmem = 1024 + kOffBars + kWarps * kStages * 8;
+  static_assert(kMergeBytes <= kRing, "the warps' results are merged in the ring");
+};
+
+SA_DEV float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+SA_DEV uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// The codes in the high / low bytes of both halves of x as a bf16 pair: a
+// code's 7 low bits are the exponent and mantissa of a bf16 2^120 times
+// smaller, subnormals included.
+constexpr uint32_t kTwo120 = 0x7b807b80u;  // (2^120, 2^120)
+SA_DEV uint32_t bf16_high_codes(uint32_t x) {
+  return mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), kTwo120);
+}
+SA_DEV uint32_t bf16_low_codes(uint32_t x) {
+  return mul_bf16x2(((x << 8) & 0x80008000u) | ((x << 4) & 0x07f007f0u), kTwo120);
+}
+
+// Tiles of a unit: tokens [0, S) and [lo, N).
+struct Unit {
+  int N, lo, S, st, wt0, nt;
+};
+SA_DEV Unit unit_of(const PagedDecodeArgs& a, int b, int* status) {
+  Unit u;
+  u.N = paged_tokens(a.p.kv, b, status);
+  u.lo = a.p.window && u.N > a.p.window ? u.N - a.p.window : 0;
+  u.S = a.p.window ? min(a.p.sinks, u.N) : 0;
+  u.wt0 = u.lo >> 4;
+  u.st = min((u.S + 15) >> 4, u.wt0);
+  u.nt = u.st + ((u.N + 15) >> 4) - u.wt0;
+  return u;
+}
+
+template <bool E4M3, int TERMS>
+__global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
+  using R = Ring<E4M3>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ long long s_scan[kWarps];
+  __shared__ long long s_plan[4];  // total, work in the first sequence before this CTA's, its index, CTAs
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gq = lane >> 2, c = lane & 3;
+  const PagedView& kv = a.p.kv;
+  const int Hkv = kv.Hkv, G = a.p.G, B = kv.B;
+  const float ninf = -__int_as_float(0x7f800000);
+  int* status = a.p.status;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + R::kOffBars) + warp * R::kStages;
+  unsigned char* ring = base + warp * (R::kStages * R::kTile);
+  unsigned char* scales = base + R::kOffScale + warp * (R::kStages * 32);
+  if (lane == 0) {
+    for (int s = 0; s < R::kStages; ++s) mbar_init(bars + s, 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    prefetch_tmap(&a.tmap_k);
+    prefetch_tmap(&a.tmap_v);
+  }
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_trigger();  // combine_kernel may be scheduled; it waits for this grid's end
+
+  // ---- this CTA's run of the work
+  auto prefix = [&](long long v, long long& total) -> long long {
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      all += s_scan[w];
+    }
+    __syncthreads();
+    total = all;
+    return before + x - v;
+  };
+  auto seq_work = [&](int b) -> long long { return b < B ? (long long)Hkv * (unit_of(a, b, status).nt + kC0) : 0; };
+  long long total = 0, w = 0, ex = 0;
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
+    long long t;
+    w = seq_work(b0 + tid);
+    ex = prefix(w, t) + total;
+    total += t;
+  }
+  const long long most = total / kMinShare;
+  const int nc = (int)(most < 1 ? 1 : (most < (long long)gridDim.x ? most : (long long)gridDim.x));
+  if ((int)blockIdx.x >= nc) {
+    if (!a.by_unit && tid == 0) a.recs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const long long w0 = total * blockIdx.x / nc, w1 = total * (blockIdx.x + 1) / nc;
+  {
+    long long run = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+      if (B > kThreads) {
+        long long t;
+        w = seq_work(b0 + tid);
+        ex = prefix(w, t) + run;
+        run += t;
+      }
+      if (w && ex <= w0 && w0 < ex + w) {
+        s_plan[0] = w0 - ex;
+        s_plan[1] = b0 + tid;
+      }
+    }
+  }
+  __syncthreads();
+  int b = (int)s_plan[1];
+  Unit u = unit_of(a, b, nullptr);
+  int g = (int)(s_plan[0] / (u.nt + kC0)), off = (int)(s_plan[0] % (u.nt + kC0));
+  long long rem = w1 - w0, at = w0 - off;  // at: where the unit's work begins
+  if (!a.by_unit && tid == 0) a.recs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  uint32_t gi = 0;  // ring position of this warp
+  bool alive = true;
+  while (rem > 0) {
+    const int cost = u.nt + kC0;
+    const int take = (int)min(rem, (long long)(cost - off));
+    const int i0 = min(max(off - kC0, 0), u.nt), i1 = min(max(off + take - kC0, 0), u.nt);
+    const bool begins = i0 == 0 && (i1 > 0 || (u.nt == 0 && off == 0));
+    if (i1 > i0 || begins) {
+      // ---- Q fragments (B operand) in the order of the reduction axis that the K fragments have
+      const bool head_ok = gq < G;
+      const __nv_bfloat16* qrow =
+          a.p.q + (size_t)b * a.p.q_row_stride + (size_t)(g * G + (head_ok ? gq : 0)) * kHeadDim;
+      uint32_t bq[16];
+      if (E4M3) {  // step s: dims 32 c + 4 s + {0, 2} and {1, 3}
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint4 x = head_ok ? ldg_nc128(qrow + 32 * c + 8 * s) : make_uint4(0u, 0u, 0u, 0u);
+          bq[4 * s] = prmt(x.x, x.y, 0x5410);
+          bq[4 * s + 1] = prmt(x.x, x.y, 0x7632);
+          bq[4 * s + 2] = prmt(x.z, x.w, 0x5410);
+          bq[4 * s + 3] = prmt(x.z, x.w, 0x7632);
+        }
+      } else {  // step s: dims 16 s + 2 c (+ 1), 16 s + 8 + 2 c (+ 1)
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          bq[2 * s] = head_ok ? __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * s + 2 * c)) : 0u;
+          bq[2 * s + 1] = head_ok ? __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * s + 8 + 2 * c)) : 0u;
+        }
+      }
+      float m0 = ninf, m1 = ninf, l0 = 0.f, l1 = 0.f;
+      float acc[8][4];
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+
+      // ---- this warp's tiles i0 + warp + 4 it; lane k keeps the pages of
+      // tiles it = 32 j + k, the next 32 looked up while these are used
+      const int n_it = max(0, (i1 - i0 - warp + kWarps - 1) / kWarps);
+      auto start_of = [&](int it) {
+        const int i = i0 + warp + kWarps * it;
+        return 16 * (i < u.st ? i : u.wt0 + i - u.st);
+      };
+      auto look = [&](int it) -> int {
+        return it < n_it ? __ldg(kv.table + (size_t)b * kv.max_pages + start_of(it) / kv.page_size) : -1;
+      };
+      int pages = look(lane), pages1 = look(32 + lane);
+      auto page_of = [&](int it, int j) { return __shfl_sync(0xffffffffu, (it >> 5) == j ? pages : pages1, it & 31); };
+      auto issue = [&](int it, int j) {  // every lane; lanes 0 .. 3 copy
+        const int page = page_of(it, j);
+        const uint32_t s = (gi + (uint32_t)it) % R::kStages;
+        unsigned char* st = ring + s * R::kTile;
+        if (page < 0 || page >= kv.n_pages) {
+          if (lane == 0) {
+            flag_status(status, SA_ERR_DEVICE_CHECK);
+            mbar_arrive(bars + s);  // nothing to load: complete the phase
+          }
+          return;
+        }
+        const int t = start_of(it), slot = t - t / kv.page_size * kv.page_size;
+        if (lane == 0) mbar_arrive_expect_tx(bars + s, R::kTile + (E4M3 ? 32 : 0));
+        __syncwarp();
+        if (E4M3) {
+          if (lane < 2)
+            tma_load_4d(st + lane * R::kBox, lane ? &a.tmap_v : &a.tmap_k, 0, slot, g, page, bars + s);
+          else if (lane < 4)
+            bulk_load(scales + s * 32 + 16 * (lane & 1),
+                      ((lane & 1) ? kv.v_scale : kv.k_scale) + scale_index(kv, page, g, slot), 16, bars + s);
+        } else if (lane < 4) {
+          tma_load_4d(st + lane * R::kBox, lane < 2 ? &a.tmap_k : &a.tmap_v, 64 * (lane & 1), slot, g, page, bars + s);
+        }
+      };
+      int issued = 0;
+      if (alive)
+        for (; issued < min(n_it, R::kStages - 1); ++issued) issue(issued, 0);
+      // ldmatrix lane addressing (bf16): matrix = lane / 8, row in matrix = lane % 8
+      const int lrow_a = (lane & 7) + 8 * ((lane >> 3) & 1), lchk_a = lane >> 4;
+      const int lrow_v = (lane & 7) + 8 * (lane >> 4), lchk_v = (lane >> 3) & 1;
+      for (int it = 0; it < n_it && alive; ++it) {
+        const int j = it >> 5;
+        __syncwarp();  // every lane is done with the stage about to be refilled
+        if (issued < n_it) {
+          issue(issued, j);
+          ++issued;
+        }
+        const uint32_t s_it = (gi + (uint32_t)it) % R::kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + s_it, ((gi + (uint32_t)it) / R::kStages) & 1u, status))) {
+          alive = false;
+          break;
+        }
+        const int page = page_of(it, j);
+        unsigned char* st = ring + s_it * R::kTile;
+        const int t0 = start_of(it);
+        if (page >= 0 && page < kv.n_pages) {
+          // visible tokens of the tile: all of them but in the first and last tiles
+          const bool edge = t0 + 16 > u.N || (t0 < u.lo && t0 + 16 > u.S);
+          bool v0 = true, v1 = true;
+          if (edge) {
+            const int ta = t0 + gq, tb = ta + 8;
+            v0 = ta < u.N && (ta < u.S || ta >= u.lo);
+            v1 = tb < u.N && (tb < u.S || tb >= u.lo);
+            if (!E4M3) {  // V rows of other tokens may hold anything: zeros before they meet a weight of 0
+              for (int x = lane; x < 256; x += 32) {
+                const int row = x >> 4, ch = x & 15, t = t0 + row;
+                if (!(t < u.N && (t < u.S || t >= u.lo)))
+                  *reinterpret_cast<uint4*>(st + (2 + (ch >> 3)) * R::kBox + swz128(row, ch & 7)) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async();
+              __syncwarp();
+            }
+          }
+          // ---- S^T = K Q^T, two chains
+          float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+          float ka = a.scale_log2, kb = a.scale_log2, va = 1.f, vb = 1.f;
+          if (E4M3) {
+            const unsigned char* sc = scales + s_it * 32;
+            ka *= __uint_as_float((uint32_t)sc[gq] << 23);
+            kb *= __uint_as_float((uint32_t)sc[gq + 8] << 23);
+            va = __uint_as_float((uint32_t)sc[16 + gq] << 23);
+            vb = __uint_as_float((uint32_t)sc[16 + gq + 8] << 23);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 x = lds128(st + swz128(gq, 2 * c + h)), y = lds128(st + swz128(gq + 8, 2 * c + h));
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = 4 * h + i;
+                mma_bf16(i & 1 ? s2 : s, bf16_low_codes(xs[i]), bf16_low_codes(ys[i]), bf16_high_codes(xs[i]),
+                         bf16_high_codes(ys[i]), bq[2 * k], bq[2 * k + 1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint32_t a0, a1, a2, a3;
+              ldsm_x4(a0, a1, a2, a3, st + (k >> 2) * R::kBox + swz128(lrow_a, 2 * (k & 3) + lchk_a));
+              mma_bf16(k & 1 ? s2 : s, a0, a1, a2, a3, bq[2 * k], bq[2 * k + 1]);
+            }
+          }
+          // tokens gq / gq + 8, heads 2 c / 2 c + 1
+          const float z0 = v0 ? (s[0] + s2[0]) * ka : ninf, z1 = v0 ? (s[1] + s2[1]) * ka : ninf;
+          const float z2 = v1 ? (s[2] + s2[2]) * kb : ninf, z3 = v1 ? (s[3] + s2[3]) * kb : ninf;
+          float mx0 = fmaxf(z0, z2), mx1 = fmaxf(z1, z3);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+          }
+          const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+          if (__any_sync(0xffffffffu, mn0 > m0 || mn1 > m1)) {
+            const float al0 = mn0 == ninf ? 1.f : fast_exp2(m0 - mn0), al1 = mn1 == ninf ? 1.f : fast_exp2(m1 - mn1);
+            m0 = mn0;
+            m1 = mn1;
+            l0 *= al0;
+            l1 *= al1;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+              acc[mt][0] *= al0;
+              acc[mt][1] *= al1;
+              acc[mt][2] *= al0;
+              acc[mt][3] *= al1;
+            }
+          }
+          const float r0 = m0 == ninf ? 0.f : -m0, r1 = m1 == ninf ? 0.f : -m1;  // nothing seen: exp2(-inf) = 0
+          float p0 = fast_exp2(z0 + r0), p1 = fast_exp2(z1 + r1), p2 = fast_exp2(z2 + r0), p3 = fast_exp2(z3 + r1);
+          l0 += p0 + p2;
+          l1 += p1 + p3;
+          if (E4M3) {  // (a scale byte of a hidden token may be anything)
+            p0 = v0 ? p0 * va : 0.f;
+            p1 = v0 ? p1 * va : 0.f;
+            p2 = v1 ? p2 * vb : 0.f;
+            p3 = v1 ? p3 * vb : 0.f;
+          }
+          // P (C layout: [token][head]) -> bf16 terms -> B layout ([head][token])
+          uint32_t bt0[TERMS], bt1[TERMS];
+#pragma unroll
+          for (int x = 0; x < TERMS; ++x) {
+            const uint32_t lo = pack_bf16(p0, p1), hi = pack_bf16(p2, p3);
+            p0 -= bf16_lo(lo);
+            p1 -= bf16_hi(lo);
+            p2 -= bf16_lo(hi);
+            p3 -= bf16_hi(hi);
+            bt0[x] = movmatrix_t(lo);
+            bt1[x] = movmatrix_t(hi);
+          }
+          // ---- O^T += V^T P^T
+          if (E4M3) {  // m-tile mt: dims 16 gq + mt and 16 gq + 8 + mt; tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+            const unsigned char* vt = st + R::kBox;
+            const uint4 x0 = lds128(vt + swz128(2 * c, gq)), x1 = lds128(vt + swz128(2 * c + 1, gq));
+            const uint4 x2 = lds128(vt + swz128(2 * c + 8, gq)), x3 = lds128(vt + swz128(2 * c + 9, gq));
+            const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+            const uint32_t w2[4] = {x2.x, x2.y, x2.z, x2.w}, w3[4] = {x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {  // byte pairs (2 y, 2 y + 1) of the 8 dims, and of the 8 after them
+              const uint32_t sel = y & 1 ? 0x7632 : 0x5410;
+              const uint32_t ta = prmt(w0[y >> 1], w1[y >> 1], sel), tb = prmt(w0[2 + (y >> 1)], w1[2 + (y >> 1)], sel);
+              const uint32_t tc = prmt(w2[y >> 1], w3[y >> 1], sel), td = prmt(w2[2 + (y >> 1)], w3[2 + (y >> 1)], sel);
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t a0 = z ? bf16_high_codes(ta) : bf16_low_codes(ta);
+                const uint32_t a1 = z ? bf16_high_codes(tb) : bf16_low_codes(tb);
+                const uint32_t a2 = z ? bf16_high_codes(tc) : bf16_low_codes(tc);
+                const uint32_t a3 = z ? bf16_high_codes(td) : bf16_low_codes(td);
+#pragma unroll
+                for (int x = 0; x < TERMS; ++x) mma_bf16(acc[2 * y + z], a0, a1, a2, a3, bt0[x], bt1[x]);
+              }
+            }
+          } else {  // m-tile mt: dims 16 mt + gq and 16 mt + 8 + gq
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+              uint32_t a0, a1, a2, a3;
+              ldsm_x4_t(a0, a1, a2, a3, st + (2 + (mt >> 2)) * R::kBox + swz128(lrow_v, 2 * (mt & 3) + lchk_v));
+#pragma unroll
+              for (int x = 0; x < TERMS; ++x) mma_bf16(acc[mt], a0, a1, a2, a3, bt0[x], bt1[x]);
+            }
+          }
+        }
+        if ((it & 31) == 31) {
+          pages = pages1;
+          pages1 = look(it + 33 + lane);
+        }
+      }
+      if (!alive) {  // the copies issued have landed before the ring goes (bounded)
+        for (int it = max(0, issued - R::kStages); it < issued; ++it)
+          mbar_wait(bars + (gi + (uint32_t)it) % R::kStages, ((gi + (uint32_t)it) / R::kStages) & 1u, nullptr);
+      }
+      gi += (uint32_t)n_it;
+
+      // ---- merge the warps in shared memory
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+      }
+      __syncthreads();  // the rings are no longer read
+      float* w_acc = reinterpret_cast<float*>(base);               // [warp][8][128]
+      float* w_ml = w_acc + kWarps * kMaxGroup * kHeadDim;         // [warp][8][2]
+      if (gq == 0) {
+        *reinterpret_cast<float4*>(w_ml + (warp * kMaxGroup + 2 * c) * 2) = make_float4(m0, l0, m1, l1);
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        const int d = E4M3 ? 16 * gq + mt : 16 * mt + gq;
+        float* h0 = w_acc + (warp * kMaxGroup + 2 * c) * kHeadDim + d;
+        h0[0] = acc[mt][0];
+        h0[kHeadDim] = acc[mt][1];
+        h0[8] = acc[mt][2];
+        h0[kHeadDim + 8] = acc[mt][3];
+      }
+      __syncthreads();
+      const int h = tid >> 4, d0 = (tid & 15) * 8;  // head and dims of this thread
+      float M = ninf, L = 0.f, A[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) A[x] = 0.f;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) M = fmaxf(M, w_ml[(y * kMaxGroup + h) * 2]);
+      if (M != ninf) {
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) {
+          const float f = fast_exp2(w_ml[(y * kMaxGroup + h) * 2] - M);
+          L += w_ml[(y * kMaxGroup + h) * 2 + 1] * f;
+          const float* src = w_acc + (y * kMaxGroup + h) * kHeadDim + d0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) A[x] += src[x] * f;
+        }
+      }
+      const bool whole = i0 == 0 && i1 == u.nt;
+      if (h < G) {
+        const size_t row = (size_t)b * a.p.Hq + (size_t)g * G + h;
+        if (!whole) {
+          float* dst = a.parts + (((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * kMaxGroup + h) * kPart;
+          *reinterpret_cast<float4*>(dst + d0) = make_float4(A[0], A[1], A[2], A[3]);
+          *reinterpret_cast<float4*>(dst + d0 + 4) = make_float4(A[4], A[5], A[6], A[7]);
+          if (d0 == 0) *reinterpret_cast<float2*>(dst + kHeadDim) = make_float2(M, L);
+        } else {
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          if (a.p.out) {
+            float* o = a.p.out + row * kHeadDim + d0;
+            *reinterpret_cast<float4*>(o) = make_float4(A[0] * inv, A[1] * inv, A[2] * inv, A[3] * inv);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(A[4] * inv, A[5] * inv, A[6] * inv, A[7] * inv);
+          } else {
+            *reinterpret_cast<uint4*>(a.p.out_bf16 + row * kHeadDim + d0) =
+                make_uint4(pack_bf16(A[0] * inv, A[1] * inv), pack_bf16(A[2] * inv, A[3] * inv),
+                           pack_bf16(A[4] * inv, A[5] * inv), pack_bf16(A[6] * inv, A[7] * inv));
+          }
+          if (a.p.lse && d0 == 0) a.p.lse[row] = L > 0.f ? M * kLn2 + logf(L) : ninf;
+        }
+      }
+      if (tid == 0 && i0 == 0) {  // whether, and up to which CTA, the unit goes on
+        int last = -1;
+        if (!whole) {
+          const long long x = at + cost - 1;
+          long long l = x * nc / total;
+          while (l + 1 < nc && total * (l + 1) / nc <= x) ++l;
+          while (l > 0 && total * l / nc > x) --l;
+          last = (int)l;
+        }
+        if (a.by_unit) a.recs[b * Hkv + g] = make_int4(last < 0 ? -1 : (int)blockIdx.x, last, b, g);
+        else if (last >= 0) a.recs[blockIdx.x] = make_int4((int)blockIdx.x, last, b, g);
+      }
+      fence_proxy_async();  // generic accesses to the ring before the next copies into it
+      __syncthreads();
+    }
+    rem -= take;
+    if (off + take == cost) {
+      at += cost;
+      off = 0;
+      if (++g == Hkv) {
+        g = 0;
+        if (++b < B) u = unit_of(a, b, nullptr);
+      }
+    } else {
+      off += take;
+    }
+  }
+}
+
+// Merge of the parts of a unit that was cut: a block per (cut unit, head); warp
+// w takes parts w, w + 8, ..., lane l dims 4 l .. 4 l + 3; the warps' results
+// are then merged in warp order.
+__global__ void __launch_bounds__(256) decode_combine_kernel(const __grid_constant__ PagedDecodeArgs a) {
+  grid_dep_wait();
+  __shared__ float s_o[8][kHeadDim];
+  __shared__ float2 s_ml[8];
+  const int G = a.p.G;
+  const int4 rec = a.recs[blockIdx.x / G];
+  if (rec.x < 0) return;
+  const int h = blockIdx.x % G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float ninf = -__int_as_float(0x7f800000);
+  const int np = rec.y - rec.x + 1;
+  float M = ninf, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 8;
+  for (int p0 = warp; p0 < np; p0 += 8 * kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int p = p0 + 8 * i;
+      const bool ok = p < np;
+      const float* src =
+          a.parts + (((size_t)(rec.x + (ok ? p : 0)) * 2 + (!ok || p == 0 ? 1 : 0)) * kMaxGroup + h) * kPart;
+      ml[i] = ok ? __ldcg(reinterpret_cast<const float2*>(src + kHeadDim)) : make_float2(ninf, 0.f);
+      v[i] = ok ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float nm = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) nm = fmaxf(nm, ml[i].x);
+    if (nm == ninf) continue;
+    const float f = fast_exp2(M - nm);
+    L *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float e = fast_exp2(ml[i].x - nm);
+      L += ml[i].y * e;
+      o.x += v[i].x * e;
+      o.y += v[i].y * e;
+      o.z += v[i].z * e;
+      o.w += v[i].w * e;
+    }
+    M = nm;
+  }
+  *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
+  if (lane == 0) s_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  if (warp) return;
+  M = ninf;
+#pragma unroll
+  for (int y = 0; y < 8; ++y) M = fmaxf(M, s_ml[y].x);
+  L = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != ninf) {
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const float e = fast_exp2(s_ml[y].x - M);
+      const float4 v = *reinterpret_cast<const float4*>(&s_o[y][4 * lane]);
+      L += s_ml[y].y * e;
+      o.x += v.x * e;
+      o.y += v.y * e;
+      o.z += v.z * e;
+      o.w += v.w * e;
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const size_t row = (size_t)rec.z * a.p.Hq + (size_t)rec.w * G + h;
+  if (a.p.out)
+    *reinterpret_cast<float4*>(a.p.out + row * kHeadDim + 4 * lane) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2*>(a.p.out_bf16 + row * kHeadDim + 4 * lane) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (a.p.lse && lane == 0) a.p.lse[row] = L > 0.f ? M * kLn2 + logf(L) : ninf;
+}
+
+template <bool E4M3, int TERMS>
+cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  auto* k = paged_decode_kernel<E4M3, TERMS>;
+  const cudaError_t e = allow_smem((const void*)k, Ring<E4M3>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, (unsigned)grid, kThreads, Ring<E4M3>::kSmem, st, a);
+}
+
+}  // namespace
+
+int paged_decode_grid(int sms) { return 3 * sms; }
+
+size_t paged_decode_part_floats() { return 2 * (size_t)kMaxGroup * kPart; }
+
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int grid, int recs, cudaStream_t st) {
+  const bool f32 = a.p.out != nullptr;
+  const cudaError_t e = a.p.kv.e4m3 ? (f32 ? launch<true, 3>(a, grid, st) : launch<true, 2>(a, grid, st))
+                                    : (f32 ? launch<false, 3>(a, grid, st) : launch<false, 2>(a, grid, st));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_combine_kernel, (unsigned)recs * a.p.G, 256, 0, st, a);
+}
+
+}  // namespace sa
