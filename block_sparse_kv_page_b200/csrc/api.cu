@@ -186,7 +186,7 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, unsigned long long rows,
 
 bool encode_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int rank,
                     const unsigned long long* dims, const unsigned long long* strides, const unsigned* box,
-                    bool swizzle) {
+                    bool swizzle, bool wide) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t d[5], s[4];
@@ -198,7 +198,8 @@ bool encode_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, 
     if (i + 1 < rank) s[i] = strides[i];
   }
   return fn(map, dt, (cuuint32_t)rank, const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

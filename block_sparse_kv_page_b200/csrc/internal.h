@@ -44,10 +44,11 @@ int device_sm_count();
 bool encode_tmap_2d(CUtensorMap* map, const void* base, unsigned long long rows, int row_bytes,
                     CUtensorMapDataType dt, int elem_bytes, int box_rows);
 // The same for `rank` <= 5 axes, innermost first: sizes, byte strides of axes 1 ..
-// rank - 1, box sizes; 128B swizzle or none.
+// rank - 1, box sizes; 128B swizzle or none; wide: L2 fetches 256 bytes at a
+// time (for rows of 256 bytes and more), else 128.
 bool encode_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int rank,
                     const unsigned long long* dims, const unsigned long long* strides, const unsigned* box,
-                    bool swizzle);
+                    bool swizzle, bool wide);
 // Opt a kernel into `bytes` of dynamic shared memory on the current device
 // (cached per device and kernel, so repeated launches skip the driver call).
 cudaError_t set_smem_attr(const void* func, size_t bytes);

@@ -21,11 +21,15 @@
 //   P: exp2 of the scaled scores in fp32, as two bf16 terms (three for fp32
 //      outputs: 2^-17 and 2^-25 of a weight), moved to the B layout;
 //   O^T [128 dims x 8 heads] += V^T P^T.
-// e4m3: codes become bf16 fragments in registers.  The order of the reduction
+// e4m3: codes become fragments in registers.  The order of the reduction
 // axis is free as long as both operands share it, so a lane takes whole 16-byte
 // pieces of a row: 32 dims of two tokens for K, 16 dims of four tokens for V,
-// free of bank conflicts under the swizzle.  The rows' scales (powers of two)
+// free of bank conflicts under the swizzle.  K's codes become f16 (one
+// conversion per pair; q is scaled per head to fit), V's bf16 (a weight times a
+// row's scale needs its range).  The rows' scales (powers of two)
 // multiply the scores and the weights, 4 values a lane instead of 256.
+#include <cuda_fp16.h>
+
 #include "paged.cuh"
 #include "internal.h"
 
@@ -43,7 +47,7 @@ template <bool E4M3>
 struct Ring {
   static constexpr int kBox = 2048;                  // 16 rows x 128 B
   static constexpr int kTile = (E4M3 ? 2 : 4) * kBox;
-  static constexpr int kStages = E4M3 ? 4 : 2;
+  static constexpr int kStages = E4M3 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kTile;
   static constexpr int kOffScale = kRing;            // [warp][stage][K 16 | V 16]
   static constexpr int kOffBars = kOffScale + (E4M3 ? kWarps * kStages * 32 : 0);
@@ -68,6 +72,25 @@ constexpr uint32_t kTwo120 = 0x7b807b80u;  // (2^120, 2^120)
 SA_DEV uint32_t bf16_high_codes(uint32_t x) {
   return mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), kTwo120);
 }
+// Two codes (the low or the high half of x) as an f16 pair: exact.
+SA_DEV uint32_t f16_of_codes(uint32_t x, bool high) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n"
+      : "=r"(r)
+      : "r"(high ? x >> 16 : x));
+  return r;
+}
+SA_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+SA_DEV uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 SA_DEV uint32_t bf16_low_codes(uint32_t x) {
   return mul_bf16x2(((x << 8) & 0x80008000u) | ((x << 4) & 0x07f007f0u), kTwo120);
 }
@@ -88,7 +111,7 @@ SA_DEV Unit unit_of(const PagedDecodeArgs& a, int b, int* status) {
 }
 
 template <bool E4M3, int TERMS>
-__global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   using R = Ring<E4M3>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ long long s_scan[kWarps];
@@ -186,16 +209,37 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       const __nv_bfloat16* qrow =
           a.p.q + (size_t)b * a.p.q_row_stride + (size_t)(g * G + (head_ok ? gq : 0)) * kHeadDim;
       uint32_t bq[16];
-      if (E4M3) {  // step s: dims 32 c + 4 s + {0, 2} and {1, 3}
+      float q_scale = 1.f;  // of head gq: its values are q * q_scale here
+      if (E4M3) {
+        // f16, as the codes become: each head's values times the power of two
+        // that brings the largest below 2^14 (f16 holds them exactly, those
+        // under 2^-28 of the largest to 2^-38 of it).  Step s: dims 32 c + 4 s
+        // + {0, 1} and {2, 3}.
+        uint4 x[4];
+        float mq = 0.f;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const uint4 x = head_ok ? ldg_nc128(qrow + 32 * c + 8 * s) : make_uint4(0u, 0u, 0u, 0u);
-          bq[4 * s] = prmt(x.x, x.y, 0x5410);
-          bq[4 * s + 1] = prmt(x.x, x.y, 0x7632);
-          bq[4 * s + 2] = prmt(x.z, x.w, 0x5410);
-          bq[4 * s + 3] = prmt(x.z, x.w, 0x7632);
+          x[s] = head_ok ? ldg_nc128(qrow + 32 * c + 8 * s) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t y[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mq = fmaxf(mq, fmaxf(fabsf(bf16_lo(y[i])), fabsf(bf16_hi(y[i]))));
         }
-      } else {  // step s: dims 16 s + 2 c (+ 1), 16 s + 8 + 2 c (+ 1)
+        mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
+        mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
+        const int e = min(253, max(1, 127 + 13 - ((int)(__float_as_uint(mq) >> 23) - 127)));
+        q_scale = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint32_t y[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bq[4 * s + i] = pack_f16(bf16_lo(y[i]) * q_scale, bf16_hi(y[i]) * q_scale);
+        }
+        q_scale = __uint_as_float((uint32_t)(254 - e) << 23);  // its inverse
+      }
+      // scores of heads 2 c, 2 c + 1 are multiplied by
+      const float zs0 = a.scale_log2 * __shfl_sync(0xffffffffu, q_scale, 8 * c);
+      const float zs1 = a.scale_log2 * __shfl_sync(0xffffffffu, q_scale, 8 * c + 4);
+      if (!E4M3) {  // step s: dims 16 s + 2 c (+ 1), 16 s + 8 + 2 c (+ 1)
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           bq[2 * s] = head_ok ? __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * s + 2 * c)) : 0u;
@@ -214,23 +258,32 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
         const int i = i0 + warp + kWarps * it;
         return 16 * (i < u.st ? i : u.wt0 + i - u.st);
       };
-      auto look = [&](int it) -> int {
-        return it < n_it ? __ldg(kv.table + (size_t)b * kv.max_pages + start_of(it) / kv.page_size) : -1;
+      const int n_pages = (int)kv.n_pages;
+      auto look = [&](int it, int& page, int& slot) {
+        page = -1;
+        slot = 0;
+        if (it < n_it) {
+          const int t = start_of(it), e = t / kv.page_size;
+          slot = t - e * kv.page_size;
+          page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
+        }
       };
-      int pages = look(lane), pages1 = look(32 + lane);
+      int pages, pages1, slots, slots1;
+      look(lane, pages, slots);
+      look(32 + lane, pages1, slots1);
       auto page_of = [&](int it, int j) { return __shfl_sync(0xffffffffu, (it >> 5) == j ? pages : pages1, it & 31); };
       auto issue = [&](int it, int j) {  // every lane; lanes 0 .. 3 copy
         const int page = page_of(it, j);
         const uint32_t s = (gi + (uint32_t)it) % R::kStages;
         unsigned char* st = ring + s * R::kTile;
-        if (page < 0 || page >= kv.n_pages) {
+        const int slot = __shfl_sync(0xffffffffu, (it >> 5) == j ? slots : slots1, it & 31);
+        if ((unsigned)page >= (unsigned)n_pages) {
           if (lane == 0) {
             flag_status(status, SA_ERR_DEVICE_CHECK);
             mbar_arrive(bars + s);  // nothing to load: complete the phase
           }
           return;
         }
-        const int t = start_of(it), slot = t - t / kv.page_size * kv.page_size;
         if (lane == 0) mbar_arrive_expect_tx(bars + s, R::kTile + (E4M3 ? 32 : 0));
         __syncwarp();
         if (E4M3) {
@@ -264,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
         const int page = page_of(it, j);
         unsigned char* st = ring + s_it * R::kTile;
         const int t0 = start_of(it);
-        if (page >= 0 && page < kv.n_pages) {
+        if ((unsigned)page < (unsigned)n_pages) {
           // visible tokens of the tile: all of them but in the first and last tiles
           const bool edge = t0 + 16 > u.N || (t0 < u.lo && t0 + 16 > u.S);
           bool v0 = true, v1 = true;
@@ -285,11 +338,11 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           }
           // ---- S^T = K Q^T, two chains
           float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-          float ka = a.scale_log2, kb = a.scale_log2, va = 1.f, vb = 1.f;
+          float ka = 1.f, kb = 1.f, va = 1.f, vb = 1.f;  // the tokens' scales
           if (E4M3) {
             const unsigned char* sc = scales + s_it * 32;
-            ka *= __uint_as_float((uint32_t)sc[gq] << 23);
-            kb *= __uint_as_float((uint32_t)sc[gq + 8] << 23);
+            ka = __uint_as_float((uint32_t)sc[gq] << 23);
+            kb = __uint_as_float((uint32_t)sc[gq + 8] << 23);
             va = __uint_as_float((uint32_t)sc[16 + gq] << 23);
             vb = __uint_as_float((uint32_t)sc[16 + gq + 8] << 23);
 #pragma unroll
@@ -299,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int k = 4 * h + i;
-                mma_bf16(i & 1 ? s2 : s, bf16_low_codes(xs[i]), bf16_low_codes(ys[i]), bf16_high_codes(xs[i]),
-                         bf16_high_codes(ys[i]), bq[2 * k], bq[2 * k + 1]);
+                mma_f16(i & 1 ? s2 : s, f16_of_codes(xs[i], false), f16_of_codes(ys[i], false),
+                        f16_of_codes(xs[i], true), f16_of_codes(ys[i], true), bq[2 * k], bq[2 * k + 1]);
               }
             }
           } else {
@@ -312,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
             }
           }
           // tokens gq / gq + 8, heads 2 c / 2 c + 1
-          const float z0 = v0 ? (s[0] + s2[0]) * ka : ninf, z1 = v0 ? (s[1] + s2[1]) * ka : ninf;
-          const float z2 = v1 ? (s[2] + s2[2]) * kb : ninf, z3 = v1 ? (s[3] + s2[3]) * kb : ninf;
+          const float z0 = v0 ? (s[0] + s2[0]) * ka * zs0 : ninf, z1 = v0 ? (s[1] + s2[1]) * ka * zs1 : ninf;
+          const float z2 = v1 ? (s[2] + s2[2]) * kb * zs0 : ninf, z3 = v1 ? (s[3] + s2[3]) * kb * zs1 : ninf;
           float mx0 = fmaxf(z0, z2), mx1 = fmaxf(z1, z3);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
@@ -391,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
         }
         if ((it & 31) == 31) {
           pages = pages1;
-          pages1 = look(it + 33 + lane);
+          slots = slots1;
+          look(it + 33 + lane, pages1, slots1);
         }
       }
       if (!alive) {  // the copies issued have landed before the ring goes (bounded)
@@ -576,7 +630,7 @@ cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-int paged_decode_grid(int sms) { return 3 * sms; }
+int paged_decode_grid(bool e4m3, int sms) { return (e4m3 ? 4 : 3) * sms; }
 
 size_t paged_decode_part_floats() { return 2 * (size_t)kMaxGroup * kPart; }
 
