@@ -154,7 +154,7 @@ sa_status decode(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   a.p = p;
   a.scale_log2 = p.scale * kLog2e;
   if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, 16, true)) return SA_ERR_CUDA;
-  const int grid = paged_decode_grid(kv.e4m3 != 0, device_sm_count());
+  const int grid = paged_decode_grid(device_sm_count());
   const long long units = (long long)kv.B * kv.Hkv;
   a.by_unit = units <= grid ? 1 : 0;
   const size_t part_bytes = align256((size_t)grid * paged_decode_part_floats() * sizeof(float));

@@ -90,7 +90,7 @@ struct PagedDecodeArgs {
   float* parts;                      // [grid][head, tail segment][8 heads][132]
   int4* recs;                        // cut units: first CTA (-1: none), last CTA, b, g
 };
-int paged_decode_grid(bool e4m3, int sms);
+int paged_decode_grid(int sms);
 size_t paged_decode_part_floats();   // per CTA
 // recs: entries of a.recs, the smaller of units and grid
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int grid, int recs, cudaStream_t st);

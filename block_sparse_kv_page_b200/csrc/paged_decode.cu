@@ -46,11 +46,12 @@ constexpr int kMergeBytes = kWarps * kMaxGroup * (kHeadDim + 2) * 4;
 template <bool E4M3>
 struct Ring {
   static constexpr int kBox = 2048;                  // 16 rows x 128 B
-  static constexpr int kTile = (E4M3 ? 2 : 4) * kBox;
-  static constexpr int kStages = E4M3 ? 3 : 2;
+  static constexpr int kSub = E4M3 ? 2 : 1;           // tiles of 16 tokens per ring stage
+  static constexpr int kTile = kSub * (E4M3 ? 2 : 4) * kBox;
+  static constexpr int kStages = 2;
   static constexpr int kRing = kWarps * kStages * kTile;
-  static constexpr int kOffScale = kRing;            // [warp][stage][K 16 | V 16]
-  static constexpr int kOffBars = kOffScale + (E4M3 ? kWarps * kStages * 32 : 0);
+  static constexpr int kOffScale = kRing;            // [warp][stage][tile][K 16 | V 16]
+  static constexpr int kOffBars = kOffScale + (E4M3 ? kWarps * kStages * kSub * 32 : 0);
   static constexpr int kSmem = 1024 + kOffBars + kWarps * kStages * 8;
   static_assert(kMergeBytes <= kRing, "the warps' results are merged in the ring");
 };
@@ -75,9 +76,10 @@ SA_DEV uint32_t bf16_high_codes(uint32_t x) {
 // Two codes (the low or the high half of x) as an f16 pair: exact.
 SA_DEV uint32_t f16_of_codes(uint32_t x, bool high) {
   uint32_t r;
-  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n"
-      : "=r"(r)
-      : "r"(high ? x >> 16 : x));
+  if (high)
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}\n" : "=r"(r) : "r"(x));
+  else
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(r) : "r"(x));
   return r;
 }
 SA_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -111,7 +113,7 @@ SA_DEV Unit unit_of(const PagedDecodeArgs& a, int b, int* status) {
 }
 
 template <bool E4M3, int TERMS>
-__global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   using R = Ring<E4M3>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ long long s_scan[kWarps];
@@ -126,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
   int* status = a.p.status;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + R::kOffBars) + warp * R::kStages;
   unsigned char* ring = base + warp * (R::kStages * R::kTile);
-  unsigned char* scales = base + R::kOffScale + warp * (R::kStages * 32);
+  unsigned char* scales = base + R::kOffScale + warp * (R::kStages * R::kSub * 32);
+  constexpr int SUB = R::kSub;
   if (lane == 0) {
     for (int s = 0; s < R::kStages; ++s) mbar_init(bars + s, 1);
     fence_barrier_init();
@@ -251,49 +254,61 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
 
-      // ---- this warp's tiles i0 + warp + 4 it; lane k keeps the pages of
-      // tiles it = 32 j + k, the next 32 looked up while these are used
-      const int n_it = max(0, (i1 - i0 - warp + kWarps - 1) / kWarps);
-      auto start_of = [&](int it) {
-        const int i = i0 + warp + kWarps * it;
-        return 16 * (i < u.st ? i : u.wt0 + i - u.st);
-      };
+      // ---- this warp's tiles, SUB at a time: i0 + SUB (warp + 4 it) + u of
+      // iteration it; lane k keeps the pages of its tiles 32 j + k (in that
+      // order), the next 32 looked up while these are used
+      const int nt = i1 - i0;
+      const int n_it = max(0, ((nt + SUB - 1) / SUB - warp + kWarps - 1) / kWarps);
+      auto tile_of = [&](int x) { return SUB * (warp + kWarps * (x / SUB)) + x % SUB; };  // in [i0, i1): < nt
+      auto start_of = [&](int i) { return 16 * (i0 + i < u.st ? i0 + i : u.wt0 + i0 + i - u.st); };
       const int n_pages = (int)kv.n_pages;
-      auto look = [&](int it, int& page, int& slot) {
-        page = -1;
+      auto look = [&](int x, int& page, int& slot) {
+        page = -2;  // no such tile
         slot = 0;
-        if (it < n_it) {
-          const int t = start_of(it), e = t / kv.page_size;
+        const int i = tile_of(x);
+        if (i < nt) {
+          const int t = start_of(i), e = t / kv.page_size;
           slot = t - e * kv.page_size;
           page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
+          if (page == -2) page = -1;
         }
       };
       int pages, pages1, slots, slots1;
       look(lane, pages, slots);
       look(32 + lane, pages1, slots1);
-      auto page_of = [&](int it, int j) { return __shfl_sync(0xffffffffu, (it >> 5) == j ? pages : pages1, it & 31); };
-      auto issue = [&](int it, int j) {  // every lane; lanes 0 .. 3 copy
-        const int page = page_of(it, j);
+      auto page_of = [&](int x, int j) { return __shfl_sync(0xffffffffu, (x >> 5) == j ? pages : pages1, x & 31); };
+      auto issue = [&](int it, int j) {  // every lane; a few of them copy
         const uint32_t s = (gi + (uint32_t)it) % R::kStages;
         unsigned char* st = ring + s * R::kTile;
-        const int slot = __shfl_sync(0xffffffffu, (it >> 5) == j ? slots : slots1, it & 31);
-        if ((unsigned)page >= (unsigned)n_pages) {
-          if (lane == 0) {
-            flag_status(status, SA_ERR_DEVICE_CHECK);
-            mbar_arrive(bars + s);  // nothing to load: complete the phase
-          }
-          return;
+        const int x0 = it * SUB;
+        int page[SUB], slot[SUB], good = 0;
+#pragma unroll
+        for (int y = 0; y < SUB; ++y) {
+          page[y] = page_of(x0 + y, j);
+          slot[y] = __shfl_sync(0xffffffffu, ((x0 + y) >> 5) == j ? slots : slots1, (x0 + y) & 31);
+          if ((unsigned)page[y] < (unsigned)n_pages) ++good;
+          else if (page[y] != -2 && lane == 0) flag_status(status, SA_ERR_DEVICE_CHECK);
         }
-        if (lane == 0) mbar_arrive_expect_tx(bars + s, R::kTile + (E4M3 ? 32 : 0));
+        if (lane == 0) {
+          if (good) mbar_arrive_expect_tx(bars + s, good * (R::kTile / SUB + (E4M3 ? 32 : 0)));
+          else mbar_arrive(bars + s);  // nothing to load: complete the phase
+        }
         __syncwarp();
-        if (E4M3) {
-          if (lane < 2)
-            tma_load_4d(st + lane * R::kBox, lane ? &a.tmap_v : &a.tmap_k, 0, slot, g, page, bars + s);
-          else if (lane < 4)
-            bulk_load(scales + s * 32 + 16 * (lane & 1),
-                      ((lane & 1) ? kv.v_scale : kv.k_scale) + scale_index(kv, page, g, slot), 16, bars + s);
-        } else if (lane < 4) {
-          tma_load_4d(st + lane * R::kBox, lane < 2 ? &a.tmap_k : &a.tmap_v, 64 * (lane & 1), slot, g, page, bars + s);
+        const int y = SUB == 1 ? 0 : lane >> 2, l = lane & 3;
+        if (lane < 4 * SUB) {
+          const int pg = y ? page[SUB - 1] : page[0], sl = y ? slot[SUB - 1] : slot[0];
+          if ((unsigned)pg < (unsigned)n_pages) {
+            unsigned char* dst = st + y * (R::kTile / SUB);
+            if (E4M3) {
+              if (l < 2)
+                tma_load_4d(dst + l * R::kBox, l ? &a.tmap_v : &a.tmap_k, 0, sl, g, pg, bars + s);
+              else
+                bulk_load(scales + (s * SUB + y) * 32 + 16 * (l & 1),
+                          ((l & 1) ? kv.v_scale : kv.k_scale) + scale_index(kv, pg, g, sl), 16, bars + s);
+            } else {
+              tma_load_4d(dst + l * R::kBox, l < 2 ? &a.tmap_k : &a.tmap_v, 64 * (l & 1), sl, g, pg, bars + s);
+            }
+          }
         }
       };
       int issued = 0;
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
       const int lrow_a = (lane & 7) + 8 * ((lane >> 3) & 1), lchk_a = lane >> 4;
       const int lrow_v = (lane & 7) + 8 * (lane >> 4), lchk_v = (lane >> 3) & 1;
       for (int it = 0; it < n_it && alive; ++it) {
-        const int j = it >> 5;
+        const int j = (it * SUB) >> 5;
         __syncwarp();  // every lane is done with the stage about to be refilled
         if (issued < n_it) {
           issue(issued, j);
@@ -314,17 +329,20 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
           alive = false;
           break;
         }
-        const int page = page_of(it, j);
-        unsigned char* st = ring + s_it * R::kTile;
-        const int t0 = start_of(it);
-        if ((unsigned)page < (unsigned)n_pages) {
+        bool good[SUB], v0[SUB], v1[SUB];
+        float z[SUB][4], va[SUB], vb[SUB];
+        float mx0 = ninf, mx1 = ninf;
+#pragma unroll
+        for (int y = 0; y < SUB; ++y) {
+          good[y] = (unsigned)page_of(it * SUB + y, j) < (unsigned)n_pages;
+          unsigned char* st = ring + s_it * R::kTile + y * (R::kTile / SUB);
           // visible tokens of the tile: all of them but in the first and last tiles
-          const bool edge = t0 + 16 > u.N || (t0 < u.lo && t0 + 16 > u.S);
-          bool v0 = true, v1 = true;
-          if (edge) {
+          const int t0 = start_of(SUB * (warp + kWarps * it) + y);
+          v0[y] = v1[y] = good[y];
+          if (good[y] && (t0 + 16 > u.N || (t0 < u.lo && t0 + 16 > u.S))) {
             const int ta = t0 + gq, tb = ta + 8;
-            v0 = ta < u.N && (ta < u.S || ta >= u.lo);
-            v1 = tb < u.N && (tb < u.S || tb >= u.lo);
+            v0[y] = ta < u.N && (ta < u.S || ta >= u.lo);
+            v1[y] = tb < u.N && (tb < u.S || tb >= u.lo);
             if (!E4M3) {  // V rows of other tokens may hold anything: zeros before they meet a weight of 0
               for (int x = lane; x < 256; x += 32) {
                 const int row = x >> 4, ch = x & 15, t = t0 + row;
@@ -336,19 +354,20 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
               __syncwarp();
             }
           }
-          // ---- S^T = K Q^T, two chains
+          // ---- S^T = K Q^T, two chains (a tile that was not loaded gives junk, which nothing sees)
           float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-          float ka = 1.f, kb = 1.f, va = 1.f, vb = 1.f;  // the tokens' scales
+          float ka = 1.f, kb = 1.f;  // the tokens' scales
+          va[y] = vb[y] = 1.f;
           if (E4M3) {
-            const unsigned char* sc = scales + s_it * 32;
+            const unsigned char* sc = scales + (s_it * SUB + y) * 32;
             ka = __uint_as_float((uint32_t)sc[gq] << 23);
             kb = __uint_as_float((uint32_t)sc[gq + 8] << 23);
-            va = __uint_as_float((uint32_t)sc[16 + gq] << 23);
-            vb = __uint_as_float((uint32_t)sc[16 + gq + 8] << 23);
+            va[y] = __uint_as_float((uint32_t)sc[16 + gq] << 23);
+            vb[y] = __uint_as_float((uint32_t)sc[16 + gq + 8] << 23);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint4 x = lds128(st + swz128(gq, 2 * c + h)), y = lds128(st + swz128(gq + 8, 2 * c + h));
-              const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+              const uint4 xk = lds128(st + swz128(gq, 2 * c + h)), yk = lds128(st + swz128(gq + 8, 2 * c + h));
+              const uint32_t xs[4] = {xk.x, xk.y, xk.z, xk.w}, ys[4] = {yk.x, yk.y, yk.z, yk.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int k = 4 * h + i;
@@ -365,38 +384,47 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
             }
           }
           // tokens gq / gq + 8, heads 2 c / 2 c + 1
-          const float z0 = v0 ? (s[0] + s2[0]) * ka * zs0 : ninf, z1 = v0 ? (s[1] + s2[1]) * ka * zs1 : ninf;
-          const float z2 = v1 ? (s[2] + s2[2]) * kb * zs0 : ninf, z3 = v1 ? (s[3] + s2[3]) * kb * zs1 : ninf;
-          float mx0 = fmaxf(z0, z2), mx1 = fmaxf(z1, z3);
+          z[y][0] = v0[y] ? (s[0] + s2[0]) * ka * zs0 : ninf;
+          z[y][1] = v0[y] ? (s[1] + s2[1]) * ka * zs1 : ninf;
+          z[y][2] = v1[y] ? (s[2] + s2[2]) * kb * zs0 : ninf;
+          z[y][3] = v1[y] ? (s[3] + s2[3]) * kb * zs1 : ninf;
+          mx0 = fmaxf(mx0, fmaxf(z[y][0], z[y][2]));
+          mx1 = fmaxf(mx1, fmaxf(z[y][1], z[y][3]));
+        }
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-          }
-          const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-          if (__any_sync(0xffffffffu, mn0 > m0 || mn1 > m1)) {
-            const float al0 = mn0 == ninf ? 1.f : fast_exp2(m0 - mn0), al1 = mn1 == ninf ? 1.f : fast_exp2(m1 - mn1);
-            m0 = mn0;
-            m1 = mn1;
-            l0 *= al0;
-            l1 *= al1;
+        for (int o = 4; o < 32; o <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        }
+        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+        if (__any_sync(0xffffffffu, mn0 > m0 || mn1 > m1)) {
+          const float al0 = mn0 == ninf ? 1.f : fast_exp2(m0 - mn0), al1 = mn1 == ninf ? 1.f : fast_exp2(m1 - mn1);
+          m0 = mn0;
+          m1 = mn1;
+          l0 *= al0;
+          l1 *= al1;
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt) {
-              acc[mt][0] *= al0;
-              acc[mt][1] *= al1;
-              acc[mt][2] *= al0;
-              acc[mt][3] *= al1;
-            }
+          for (int mt = 0; mt < 8; ++mt) {
+            acc[mt][0] *= al0;
+            acc[mt][1] *= al1;
+            acc[mt][2] *= al0;
+            acc[mt][3] *= al1;
           }
-          const float r0 = m0 == ninf ? 0.f : -m0, r1 = m1 == ninf ? 0.f : -m1;  // nothing seen: exp2(-inf) = 0
-          float p0 = fast_exp2(z0 + r0), p1 = fast_exp2(z1 + r1), p2 = fast_exp2(z2 + r0), p3 = fast_exp2(z3 + r1);
+        }
+        const float r0 = m0 == ninf ? 0.f : -m0, r1 = m1 == ninf ? 0.f : -m1;  // nothing seen: exp2(-inf) = 0
+#pragma unroll
+        for (int y = 0; y < SUB; ++y) {
+          if (!good[y]) continue;
+          unsigned char* st = ring + s_it * R::kTile + y * (R::kTile / SUB);
+          float p0 = fast_exp2(z[y][0] + r0), p1 = fast_exp2(z[y][1] + r1);
+          float p2 = fast_exp2(z[y][2] + r0), p3 = fast_exp2(z[y][3] + r1);
           l0 += p0 + p2;
           l1 += p1 + p3;
           if (E4M3) {  // (a scale byte of a hidden token may be anything)
-            p0 = v0 ? p0 * va : 0.f;
-            p1 = v0 ? p1 * va : 0.f;
-            p2 = v1 ? p2 * vb : 0.f;
-            p3 = v1 ? p3 * vb : 0.f;
+            p0 = v0[y] ? p0 * va[y] : 0.f;
+            p1 = v0[y] ? p1 * va[y] : 0.f;
+            p2 = v1[y] ? p2 * vb[y] : 0.f;
+            p3 = v1[y] ? p3 * vb[y] : 0.f;
           }
           // P (C layout: [token][head]) -> bf16 terms -> B layout ([head][token])
           uint32_t bt0[TERMS], bt1[TERMS];
@@ -418,18 +446,18 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
             const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
             const uint32_t w2[4] = {x2.x, x2.y, x2.z, x2.w}, w3[4] = {x3.x, x3.y, x3.z, x3.w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {  // byte pairs (2 y, 2 y + 1) of the 8 dims, and of the 8 after them
-              const uint32_t sel = y & 1 ? 0x7632 : 0x5410;
-              const uint32_t ta = prmt(w0[y >> 1], w1[y >> 1], sel), tb = prmt(w0[2 + (y >> 1)], w1[2 + (y >> 1)], sel);
-              const uint32_t tc = prmt(w2[y >> 1], w3[y >> 1], sel), td = prmt(w2[2 + (y >> 1)], w3[2 + (y >> 1)], sel);
+            for (int i = 0; i < 4; ++i) {  // byte pairs (2 i, 2 i + 1) of the 8 dims, and of the 8 after them
+              const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
+              const uint32_t ta = prmt(w0[i >> 1], w1[i >> 1], sel), tb = prmt(w0[2 + (i >> 1)], w1[2 + (i >> 1)], sel);
+              const uint32_t tc = prmt(w2[i >> 1], w3[i >> 1], sel), td = prmt(w2[2 + (i >> 1)], w3[2 + (i >> 1)], sel);
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const uint32_t a0 = z ? bf16_high_codes(ta) : bf16_low_codes(ta);
-                const uint32_t a1 = z ? bf16_high_codes(tb) : bf16_low_codes(tb);
-                const uint32_t a2 = z ? bf16_high_codes(tc) : bf16_low_codes(tc);
-                const uint32_t a3 = z ? bf16_high_codes(td) : bf16_low_codes(td);
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t a0 = k ? bf16_high_codes(ta) : bf16_low_codes(ta);
+                const uint32_t a1 = k ? bf16_high_codes(tb) : bf16_low_codes(tb);
+                const uint32_t a2 = k ? bf16_high_codes(tc) : bf16_low_codes(tc);
+                const uint32_t a3 = k ? bf16_high_codes(td) : bf16_low_codes(td);
 #pragma unroll
-                for (int x = 0; x < TERMS; ++x) mma_bf16(acc[2 * y + z], a0, a1, a2, a3, bt0[x], bt1[x]);
+                for (int x = 0; x < TERMS; ++x) mma_bf16(acc[2 * i + k], a0, a1, a2, a3, bt0[x], bt1[x]);
               }
             }
           } else {  // m-tile mt: dims 16 mt + gq and 16 mt + 8 + gq
@@ -442,10 +470,10 @@ __global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3) paged_decode_kernel(co
             }
           }
         }
-        if ((it & 31) == 31) {
+        if (((it * SUB) & 31) == 32 - SUB) {
           pages = pages1;
           slots = slots1;
-          look(it + 33 + lane, pages1, slots1);
+          look(it * SUB + SUB + 32 + lane, pages1, slots1);
         }
       }
       if (!alive) {  // the copies issued have landed before the ring goes (bounded)
@@ -630,7 +658,7 @@ cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-int paged_decode_grid(bool e4m3, int sms) { return (e4m3 ? 4 : 3) * sms; }
+int paged_decode_grid(int sms) { return 3 * sms; }
 
 size_t paged_decode_part_floats() { return 2 * (size_t)kMaxGroup * kPart; }
 
