@@ -24,9 +24,11 @@
 // e4m3: codes become fragments in registers.  The order of the reduction
 // axis is free as long as both operands share it, so a lane takes whole 16-byte
 // pieces of a row: 32 dims of two tokens for K, 16 dims of four tokens for V,
-// free of bank conflicts under the swizzle.  K's codes become f16 (one
-// conversion per pair; q is scaled per head to fit), V's bf16 (a weight times a
-// row's scale needs its range).  The rows' scales (powers of two)
+// free of bank conflicts under the swizzle.  Codes become f16, one conversion per
+// pair: q is scaled per head to fit, and weights times V's scales are taken
+// relative to the largest scale seen, which is followed like the maximum; rows
+// whose scale lies far below it take the same products in bf16 (whose
+// conversion, by shifts and masks, costs three times as much).  The rows' scales (powers of two)
 // multiply the scores and the weights, 4 values a lane instead of 256.
 #include <cuda_fp16.h>
 
@@ -130,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
   unsigned char* ring = base + warp * (R::kStages * R::kTile);
   unsigned char* scales = base + R::kOffScale + warp * (R::kStages * R::kSub * 32);
   constexpr int SUB = R::kSub;
+  constexpr int kNear = TERMS == 3 ? 2 : 8;  // binary places between the largest V scale and one for f16 weights
   if (lane == 0) {
     for (int s = 0; s < R::kStages; ++s) mbar_init(bars + s, 1);
     fence_barrier_init();
@@ -253,6 +256,9 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       float acc[8][4];
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+      // e4m3: acc is held in units of 2^(e_acc - 127), the largest V scale byte
+      // of a visible token so far, so that weight * scale is at most 1
+      int e_acc = -1000;
 
       // ---- this warp's tiles, SUB at a time: i0 + SUB (warp + 4 it) + u of
       // iteration it; lane k keeps the pages of its tiles 32 j + k (in that
@@ -329,8 +335,9 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           alive = false;
           break;
         }
-        bool good[SUB], v0[SUB], v1[SUB];
-        float z[SUB][4], va[SUB], vb[SUB];
+        bool good[SUB], edge[SUB], v0[SUB], v1[SUB];
+        float z[SUB][4];
+        int ea[SUB], eb[SUB];  // V scale bytes of this lane's tokens
         float mx0 = ninf, mx1 = ninf;
 #pragma unroll
         for (int y = 0; y < SUB; ++y) {
@@ -339,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           // visible tokens of the tile: all of them but in the first and last tiles
           const int t0 = start_of(SUB * (warp + kWarps * it) + y);
           v0[y] = v1[y] = good[y];
-          if (good[y] && (t0 + 16 > u.N || (t0 < u.lo && t0 + 16 > u.S))) {
+          edge[y] = good[y] && (t0 + 16 > u.N || (t0 < u.lo && t0 + 16 > u.S));
+          if (edge[y]) {
             const int ta = t0 + gq, tb = ta + 8;
             v0[y] = ta < u.N && (ta < u.S || ta >= u.lo);
             v1[y] = tb < u.N && (tb < u.S || tb >= u.lo);
@@ -357,13 +365,12 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           // ---- S^T = K Q^T, two chains (a tile that was not loaded gives junk, which nothing sees)
           float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
           float ka = 1.f, kb = 1.f;  // the tokens' scales
-          va[y] = vb[y] = 1.f;
           if (E4M3) {
             const unsigned char* sc = scales + (s_it * SUB + y) * 32;
             ka = __uint_as_float((uint32_t)sc[gq] << 23);
             kb = __uint_as_float((uint32_t)sc[gq + 8] << 23);
-            va[y] = __uint_as_float((uint32_t)sc[16 + gq] << 23);
-            vb[y] = __uint_as_float((uint32_t)sc[16 + gq + 8] << 23);
+            ea[y] = sc[16 + gq];
+            eb[y] = sc[16 + gq + 8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint4 xk = lds128(st + swz128(gq, 2 * c + h)), yk = lds128(st + swz128(gq + 8, 2 * c + h));
@@ -412,6 +419,29 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           }
         }
         const float r0 = m0 == ninf ? 0.f : -m0, r1 = m1 == ninf ? 0.f : -m1;  // nothing seen: exp2(-inf) = 0
+        bool near = false;  // every scale is near enough to the largest for f16 weights
+        if (E4M3) {
+          int hi = -1000, lo = 1000;
+#pragma unroll
+          for (int y = 0; y < SUB; ++y) {
+            hi = max(hi, max(v0[y] ? ea[y] : -1000, v1[y] ? eb[y] : -1000));
+            lo = min(lo, min(v0[y] ? ea[y] : 1000, v1[y] ? eb[y] : 1000));
+          }
+          hi = __reduce_max_sync(0xffffffffu, hi);
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          if (hi > e_acc) {
+            const float f = e_acc < hi - 126 ? 0.f : __uint_as_float((uint32_t)(127 + e_acc - hi) << 23);
+            e_acc = hi;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+              acc[mt][0] *= f;
+              acc[mt][1] *= f;
+              acc[mt][2] *= f;
+              acc[mt][3] *= f;
+            }
+          }
+          near = lo >= e_acc - kNear;
+        }
 #pragma unroll
         for (int y = 0; y < SUB; ++y) {
           if (!good[y]) continue;
@@ -420,11 +450,52 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           float p2 = fast_exp2(z[y][2] + r0), p3 = fast_exp2(z[y][3] + r1);
           l0 += p0 + p2;
           l1 += p1 + p3;
-          if (E4M3) {  // (a scale byte of a hidden token may be anything)
-            p0 = v0[y] ? p0 * va[y] : 0.f;
-            p1 = v0[y] ? p1 * va[y] : 0.f;
-            p2 = v1[y] ? p2 * vb[y] : 0.f;
-            p3 = v1[y] ? p3 * vb[y] : 0.f;
+          if (E4M3) {  // times 2^(scale - e_acc); a scale byte of a hidden token may be anything
+            const float fa = v0[y] ? __uint_as_float((uint32_t)max(0, 127 + ea[y] - e_acc) << 23) : 0.f;
+            const float fb = v1[y] ? __uint_as_float((uint32_t)max(0, 127 + eb[y] - e_acc) << 23) : 0.f;
+            p0 *= fa;
+            p1 *= fa;
+            p2 *= fb;
+            p3 *= fb;
+          }
+          if (E4M3 && near && !edge[y]) {
+            // Weights and codes in f16.  fp32 outputs: two terms, 2^-23 of a
+            // weight or 2^-25 of the largest; bf16 outputs: one, 2^-12 (the
+            // output's own rounding is 2^-9).
+            constexpr int FT = TERMS == 3 ? 2 : 1;
+            uint32_t bt0[FT], bt1[FT];
+#pragma unroll
+            for (int x = 0; x < FT; ++x) {
+              const __half2 lo = __floats2half2_rn(p0, p1), hi = __floats2half2_rn(p2, p3);
+              if (x + 1 < FT) {
+                p0 -= __low2float(lo);
+                p1 -= __high2float(lo);
+                p2 -= __low2float(hi);
+                p3 -= __high2float(hi);
+              }
+              bt0[x] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&lo));
+              bt1[x] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&hi));
+            }
+            // m-tile mt: dims 16 gq + mt and 16 gq + 8 + mt; tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+            const unsigned char* vt = st + R::kBox;
+            const uint4 x0 = lds128(vt + swz128(2 * c, gq)), x1 = lds128(vt + swz128(2 * c + 1, gq));
+            const uint4 x2 = lds128(vt + swz128(2 * c + 8, gq)), x3 = lds128(vt + swz128(2 * c + 9, gq));
+            const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+            const uint32_t w2[4] = {x2.x, x2.y, x2.z, x2.w}, w3[4] = {x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // bytes 2 i and 2 i + 1 of both tokens, side by side
+              const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
+              const uint32_t ta = prmt(w0[i >> 1], w1[i >> 1], sel), tb = prmt(w0[2 + (i >> 1)], w1[2 + (i >> 1)], sel);
+              const uint32_t tc = prmt(w2[i >> 1], w3[i >> 1], sel), td = prmt(w2[2 + (i >> 1)], w3[2 + (i >> 1)], sel);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t a0 = f16_of_codes(ta, k), a1 = f16_of_codes(tb, k);
+                const uint32_t a2 = f16_of_codes(tc, k), a3 = f16_of_codes(td, k);
+#pragma unroll
+                for (int x = 0; x < FT; ++x) mma_f16(acc[2 * i + k], a0, a1, a2, a3, bt0[x], bt1[x]);
+              }
+            }
+            continue;
           }
           // P (C layout: [token][head]) -> bf16 terms -> B layout ([head][token])
           uint32_t bt0[TERMS], bt1[TERMS];
@@ -439,7 +510,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
             bt1[x] = movmatrix_t(hi);
           }
           // ---- O^T += V^T P^T
-          if (E4M3) {  // m-tile mt: dims 16 gq + mt and 16 gq + 8 + mt; tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+          if (E4M3) {  // as above, in bf16: for a scale far below the largest, which needs its range, and
+                       // where tokens are hidden, whose codes may be NaN (here they become numbers)
             const unsigned char* vt = st + R::kBox;
             const uint4 x0 = lds128(vt + swz128(2 * c, gq)), x1 = lds128(vt + swz128(2 * c + 1, gq));
             const uint4 x2 = lds128(vt + swz128(2 * c + 8, gq)), x3 = lds128(vt + swz128(2 * c + 9, gq));
@@ -481,6 +553,17 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           mbar_wait(bars + (gi + (uint32_t)it) % R::kStages, ((gi + (uint32_t)it) / R::kStages) & 1u, nullptr);
       }
       gi += (uint32_t)n_it;
+
+      if (E4M3) {  // acc in its own units again
+        const float f = e_acc < 0 ? 0.f : __uint_as_float((uint32_t)e_acc << 23);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          acc[mt][0] *= f;
+          acc[mt][1] *= f;
+          acc[mt][2] *= f;
+          acc[mt][3] *= f;
+        }
+      }
 
       // ---- merge the warps in shared memory
 #pragma unroll
