@@ -399,7 +399,7 @@ class PagedCache:
             if e4m3 and (t.dtype != torch.uint8 or tuple(t.shape) != (n_pages, Hkv, page_size)
                          or not t.is_contiguous()):
                 raise ValueError(f"{name} must be contiguous uint8 [n_pages, Hkv, page_size]")
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         for t in (v, page_table, seq_len, k_scale, v_scale):
             if t is not None and t.device != self.device:
                 raise ValueError("the tensors of a cache must be on one device")
@@ -409,26 +409,27 @@ class PagedCache:
         self.desc = sa_paged_desc(B, Hkv, D, page_size, n_pages, _abi.SA_KV_E4M3 if e4m3 else _abi.SA_KV_BF16,
                                   max_pages, k.data_ptr(), v.data_ptr(), page_stride, head_stride, token_stride,
                                   _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), seq_len.data_ptr())
+        self.ref = C.byref(self.desc)
 
 
-def _on(kv: PagedCache, stream, tensors) -> int:
+def _on(kv: PagedCache, stream, *tensors) -> int:
     """The stream of a call on the cache's device: the given one, or that
     device's current one.  All tensors of a call are on that device."""
-    dev = kv.device
+    index = kv.index
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("the tensors of a call must be on the cache's device")
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
 
 
 def _paged_call(kv: PagedCache, fn, where: str, *args) -> None:
     """Run a call with the cache's device current."""
-    if kv.device.index == torch.cuda.current_device():
+    if kv.index == torch._C._cuda_getDevice():
         st = fn(*args)
     else:
-        with torch.cuda.device(kv.device):
+        with torch.cuda.device(kv.index):
             st = fn(*args)
     if st != 0:
         raise SparseAttnError(st, where)
@@ -456,7 +457,7 @@ def _ws(ws: torch.Tensor | None) -> tuple[int | None, int]:
 
 
 def sparse_attn_paged_workspace_size(kv: PagedCache, n_q_heads: int) -> int:
-    return int(lib.sparse_attn_paged_workspace_size(C.byref(kv.desc), int(n_q_heads)))
+    return int(lib.sparse_attn_paged_workspace_size(kv.ref, int(n_q_heads)))
 
 
 def make_paged_workspace(kv: PagedCache, n_q_heads: int, stream=None) -> torch.Tensor:
@@ -467,7 +468,7 @@ def make_paged_workspace(kv: PagedCache, n_q_heads: int, stream=None) -> torch.T
         raise SparseAttnError(_abi.SA_ERR_INVALID, "sparse_attn_paged_workspace_size")
     ws = torch.empty(n, dtype=torch.uint8, device=kv.device)
     _paged_call(kv, lib.sparse_attn_workspace_init, "sparse_attn_workspace_init", ws.data_ptr(), n,
-                _on(kv, stream, ()))
+                _on(kv, stream))
     return ws
 
 
@@ -481,10 +482,10 @@ def sparse_attn_cache_write(kv: PagedCache, k_new: torch.Tensor, v_new: torch.Te
     if v_new.shape[0] != k_new.shape[0] or _rows(v_new, "v_new", Hkv) != stride:
         raise ValueError("k_new and v_new must have the same rows and strides")
     _row_off(row_off, kv)
-    s = _on(kv, stream, (k_new, v_new, row_off, ws))
+    s = _on(kv, stream, k_new, v_new, row_off, ws)
     if k_new.shape[0] == 0:
         return
-    _paged_call(kv, lib.sparse_attn_cache_write, "sparse_attn_cache_write", C.byref(kv.desc), k_new.data_ptr(),
+    _paged_call(kv, lib.sparse_attn_cache_write, "sparse_attn_cache_write", kv.ref, k_new.data_ptr(),
                 v_new.data_ptr(), stride, row_off.data_ptr(), k_new.shape[0], *_ws(ws), s)
 
 
@@ -497,8 +498,8 @@ def sparse_attn_cache_read(kv: PagedCache, first_token: int, k_out: torch.Tensor
         if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous() or t.shape != k_out.shape \
                 or t.shape[0] != kv.batch or t.shape[1] != kv.n_kv_heads or t.shape[3] != 128:
             raise ValueError(f"{name} must be a contiguous bf16 [B, Hkv, cap, 128] tensor")
-    s = _on(kv, stream, (k_out, v_out, ws))
-    _paged_call(kv, lib.sparse_attn_cache_read, "sparse_attn_cache_read", C.byref(kv.desc), int(first_token),
+    s = _on(kv, stream, k_out, v_out, ws)
+    _paged_call(kv, lib.sparse_attn_cache_read, "sparse_attn_cache_read", kv.ref, int(first_token),
                 k_out.data_ptr(), v_out.data_ptr(), k_out.shape[2], *_ws(ws), s)
 
 
@@ -519,10 +520,10 @@ def sparse_attn_chunk(kv: PagedCache, q: torch.Tensor, row_off: torch.Tensor, sc
     stride = _rows(q, "q")
     out_dtype = _attn_out(q, out, lse)
     _row_off(row_off, kv)
-    s = _on(kv, stream, (q, row_off, out, lse, ws))
+    s = _on(kv, stream, q, row_off, out, lse, ws)
     if q.shape[0] == 0:
         return
-    _paged_call(kv, lib.sparse_attn_chunk, "sparse_attn_chunk", C.byref(kv.desc), q.data_ptr(), stride, q.shape[1],
+    _paged_call(kv, lib.sparse_attn_chunk, "sparse_attn_chunk", kv.ref, q.data_ptr(), stride, q.shape[1],
                 row_off.data_ptr(), q.shape[0], int(window), int(sinks), float(scale), out.data_ptr(), out_dtype,
                 _ptr(lse), *_ws(ws), s)
 
@@ -535,6 +536,6 @@ def sparse_attn_paged_decode(kv: PagedCache, q: torch.Tensor, scale: float, wind
     if q.shape[0] != kv.batch:
         raise ValueError("q must have one row per sequence")
     out_dtype = _attn_out(q, out, lse)
-    s = _on(kv, stream, (q, out, lse, ws))
-    _paged_call(kv, lib.sparse_attn_paged_decode, "sparse_attn_paged_decode", C.byref(kv.desc), q.data_ptr(), stride,
+    s = _on(kv, stream, q, out, lse, ws)
+    _paged_call(kv, lib.sparse_attn_paged_decode, "sparse_attn_paged_decode", kv.ref, q.data_ptr(), stride,
                 q.shape[1], int(window), int(sinks), float(scale), out.data_ptr(), out_dtype, _ptr(lse), *_ws(ws), s)
