@@ -46,7 +46,7 @@
 //                    wait on a barrier costs 200 cycles even when it is over;
 //                    one thread per slot for both products took 2490 cycles per
 //                    64 tokens, the three take about 1600.);
-//   warps 20-23      (e4m3 cache) turn the codes of K and V, fetched into a
+//   warps 20-23, 24-27 (e4m3 cache) turn the codes of K, of V, fetched into a
 //                    ring of their own, into bf16 tiles: code * 2^k is exactly
 //                    a bf16, so the products are those of a bf16 cache of the
 //                    rounded values.
@@ -256,7 +256,7 @@ SA_DEV unsigned long long scan64(unsigned long long v, unsigned long long* scrat
   return base + x - v;
 }
 
-// This CTA's share of the work (every thread calls it; scratch: 26 words).
+// This CTA's share of the work (every thread calls it; scratch: 30 words).
 SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratch) {
   const int T = blockDim.x, tid = threadIdx.x, B = a.p.kv.B;
   const unsigned long long H = a.p.kv.Hkv;
@@ -289,13 +289,13 @@ SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratc
     }
     if (w && ex <= w0 && w0 < ex + w) {
       plan->b = base + tid;
-      scratch[24] = w0 - ex;
-      scratch[25] = w / H;
+      scratch[28] = w0 - ex;
+      scratch[29] = w / H;
     }
   }
   __syncthreads();
   if (tid < 32) {
-    const unsigned long long in = scratch[24], per = scratch[25];
+    const unsigned long long in = scratch[28], per = scratch[29];
     const int b = plan->b, g = (int)(in / per);
     const unsigned long long off = in - (unsigned long long)g * per;
     int r0;
@@ -363,13 +363,13 @@ SA_DEV float max3(float a, float b, float c) {
 }
 
 template <bool E4M3, int TERMS>
-__global__ void __launch_bounds__(E4M3 ? 768 : 640, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using Sh = Shape<TERMS>;
   constexpr int NS = Sh::NS, NB = Sh::NB;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Plan s_plan;
-  __shared__ unsigned long long s_scan[26];
+  __shared__ unsigned long long s_scan[30];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* qs = base;
@@ -610,8 +610,9 @@ __global__ void __launch_bounds__(E4M3 ? 768 : 640, 1) chunk_kernel(const __grid
   } else if (warp >= 20) {
     // ---- e4m3 -> bf16: 8 threads per row, 16 rows at a time
     if constexpr (E4M3) {
-      reg_dealloc<72>();
-      const int x = tid - 640, c = x & 7, r16 = x >> 3;
+      reg_dealloc<48>();
+      const int w = (warp - 20) >> 2;  // K or V
+      const int x = (tid - 640) & 127, c = x & 7, r16 = x >> 3;
       int n = 0;
       bool ok = true;
       while (ok && cur.next(a, sg)) {
@@ -621,8 +622,7 @@ __global__ void __launch_bounds__(E4M3 ? 768 : 640, 1) chunk_kernel(const __grid
           const bool edge = kb0 + BLK > sg.p1 + 1 || (kb0 < sg.lo && kb0 + BLK > sg.S);
           const int ks = (2 * n) % NS;
           const uint32_t use = (uint32_t)((2 * n) / NS);
-#pragma unroll 1
-          for (int w = 0; w < 2 && ok; ++w) {
+          {
             const int rs = (2 * n + w) % NR;
             ok = mbar_wait(raw_full + rs, (uint32_t)((2 * n + w) / NR) & 1u, status);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -929,57 +929,56 @@ __global__ void __launch_bounds__(E4M3 ? 768 : 640, 1) chunk_kernel(const __grid
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
-// Merge of the partial results of the pairs that were cut: block x / 8 looks
-// after the pair that CTA x / 8 began, a warp after four of its 256 vectors,
-// lane l after dims 4 l .. 4 l + 3; parts in CTA order.
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ ChunkArgs a) {
+// Merge of the partial results of the pairs that were cut: a task is eight
+// vectors of the pair that one CTA began, a warp takes one of them, lane l its
+// dims 4 l .. 4 l + 3; parts in CTA order.  Tasks go round the grid, so that the
+// few pairs of a short chunk over a long cache (many parts each) use every SM.
+constexpr int kCombineThreads = 256;
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ ChunkArgs a, int ctas) {
   grid_dep_wait();
-  const int c0 = blockIdx.x >> 3;
-  const ChunkRec rec = a.recs[c0];
-  if (rec.rows <= 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float ninf = -__int_as_float(0x7f800000);
   const int G = a.p.G, R = a.R;
-  for (int i = 0; i < 4; ++i) {
-    const int v = (blockIdx.x & 7) * 32 + warp * 4 + i;
+  for (int task = blockIdx.x; task < ctas * 32; task += gridDim.x) {
+    const int c0 = task >> 5;
+    const ChunkRec rec = a.recs[c0];
+    if (rec.rows <= 0) continue;
+    const int v = (task & 31) * 8 + warp;
     const int t = v >> 7, r = v & 127;
     const int rr = r / G, row = t * R + rr;
     if (r >= G * R || row >= rec.rows || (rec.single && t)) continue;
     float M = ninf, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const int np = rec.last - c0 + 1;
-    for (int p0 = 0; p0 < np; p0 += 32) {
-      const int p = p0 + lane;
-      float2 ml = make_float2(ninf, 0.f);
-      if (p < np)
-        ml = __ldcg(reinterpret_cast<const float2*>(
-            a.parts + ((((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart + kHeadDim));
-      float mm = ml.x;
+    constexpr int kBatch = 16;
+    for (int p0 = 0; p0 < np; p0 += kBatch) {
+      float2 ml[kBatch];
+      float4 y[kBatch];
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
-      const float nm = fmaxf(M, mm);
-      if (nm == ninf) continue;
-      const float f = fast_exp2(M - nm), w = fast_exp2(ml.x - nm);
-      float lw = ml.y * w;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
-      L = L * f + lw;
-      o.x *= f;
-      o.y *= f;
-      o.z *= f;
-      o.w *= f;
-      M = nm;
-      const int cntp = min(32, np - p0);
-#pragma unroll 8
-      for (int q = 0; q < cntp; ++q) {
-        const float wq = __shfl_sync(0xffffffffu, w, q);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(
-            a.parts + ((((size_t)(c0 + p0 + q) * 2 + (p0 + q == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart + 4 * lane));
-        o.x += y.x * wq;
-        o.y += y.y * wq;
-        o.z += y.z * wq;
-        o.w += y.w * wq;
+      for (int i = 0; i < kBatch; ++i) {
+        const int p = p0 + i;
+        const bool ok = p < np;
+        const float* src = a.parts + ((((size_t)(c0 + (ok ? p : 0)) * 2 + (!ok || p == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart;
+        ml[i] = ok ? __ldcg(reinterpret_cast<const float2*>(src + kHeadDim)) : make_float2(ninf, 0.f);
+        y[i] = ok ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      float nm = M;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) nm = fmaxf(nm, ml[i].x);
+      if (nm == ninf) continue;
+      const float f = fast_exp2(M - nm);
+      L *= f;
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float w = fast_exp2(ml[i].x - nm);
+        L += ml[i].y * w;
+        o.x += y[i].x * w;
+        o.y += y[i].y * w;
+        o.z += y[i].z * w;
+        o.w += y[i].w * w;
+      }
+      M = nm;
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     const size_t orow = (size_t)(rec.row0 + row) * a.p.Hq + (size_t)rec.g * G + (r - rr * G);
@@ -999,7 +998,7 @@ cudaError_t launch(const ChunkArgs& a, int grid, cudaStream_t st) {
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const cudaError_t e = allow_smem((const void*)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, (unsigned)grid, E4M3 ? 768 : 640, smem, st, a);
+  return launch_pdl(k, (unsigned)grid, E4M3 ? 896 : 640, smem, st, a);
 }
 
 }  // namespace
@@ -1011,7 +1010,7 @@ cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st) {
   const cudaError_t e = a.p.kv.e4m3 ? (f32 ? launch<true, 3>(a, grid, st) : launch<true, 1>(a, grid, st))
                                     : (f32 ? launch<false, 3>(a, grid, st) : launch<false, 1>(a, grid, st));
   if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel, (unsigned)grid * 8, 256, 0, st, a);
+  return launch_pdl(combine_kernel, (unsigned)grid * 4, kCombineThreads, 0, st, a, grid);
 }
 
 }  // namespace sa
