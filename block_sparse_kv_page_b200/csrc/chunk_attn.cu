@@ -108,6 +108,9 @@ SA_DEV bool pair_any(int id, bool v) {
       : "memory");
   return r != 0;
 }
+// The lowest n bits, n clipped to [0, 32].
+SA_DEV uint32_t first_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
 SA_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
 
 SA_DEV float fast_exp2(float x) {
@@ -153,8 +156,15 @@ struct Seg : Geom {
 };
 
 struct Plan {
-  int b, g, j, off, n_cta;
-  unsigned long long w0, w1, total;
+  int b, g, j, off;
+  unsigned more;
+  unsigned long long w0, w1, each;
+  // The CTA that has unit x of the work.
+  SA_DEV int cta_of(unsigned long long x) const {
+    const unsigned long long longer = (each + 1) * more;
+    if (x < longer) return (int)(x / (each + 1));
+    return (int)(more + (x - longer) / each);
+  }
 };
 
 // Walks the segments of a CTA; every role has its own.
@@ -260,20 +270,23 @@ SA_DEV unsigned long long scan64(unsigned long long v, unsigned long long* scrat
 SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratch) {
   const int T = blockDim.x, tid = threadIdx.x, B = a.p.kv.B;
   const unsigned long long H = a.p.kv.Hkv;
-  unsigned long long total = 0, w = 0, t, ex = 0;
+  unsigned long long total = 0, w = 0, w1 = 0, t, ex = 0;
   for (int base = 0; base < B; base += T) {
-    w = seq_work(a, base + tid) * H;
+    w1 = seq_work(a, base + tid);
+    w = w1 * H;
     ex = scan64(w, scratch, t) + total;
     total += t;
   }
-  const unsigned long long most = total / kMinShare;
-  const unsigned long long n = most < 1 ? 1 : (most < gridDim.x ? most : gridDim.x);
-  const unsigned long long c = blockIdx.x;
+  // as many CTAs as have kMinShare each; the first `more` of them take one unit more than `each`
+  const unsigned n = total >= (unsigned long long)gridDim.x * kMinShare ? gridDim.x : max(1u, (unsigned)total / kMinShare);
+  const unsigned c = blockIdx.x;
+  const unsigned long long each = total >> 32 ? total / n : (unsigned)total / n;
+  const unsigned more = (unsigned)(total - each * n);
   if (tid == 0) {
-    plan->total = total;
-    plan->n_cta = (int)n;
-    plan->w0 = c < n ? total * c / n : 0;
-    plan->w1 = c < n ? total * (c + 1) / n : 0;
+    plan->each = each;
+    plan->more = more;
+    plan->w0 = c < n ? each * c + min(c, more) : 0;
+    plan->w1 = c < n ? plan->w0 + each + (c < more ? 1u : 0u) : 0;
     plan->b = B;
     plan->g = plan->j = plan->off = 0;
   }
@@ -283,20 +296,21 @@ SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratc
   unsigned long long run = 0;
   for (int base = 0; base < B; base += T) {
     if (B > T) {
-      w = seq_work(a, base + tid) * H;
+      w1 = seq_work(a, base + tid);
+      w = w1 * H;
       ex = scan64(w, scratch, t) + run;
       run += t;
     }
     if (w && ex <= w0 && w0 < ex + w) {
       plan->b = base + tid;
       scratch[28] = w0 - ex;
-      scratch[29] = w / H;
+      scratch[29] = w1;
     }
   }
   __syncthreads();
   if (tid < 32) {
     const unsigned long long in = scratch[28], per = scratch[29];
-    const int b = plan->b, g = (int)(in / per);
+    const int b = plan->b, g = (in >> 32) || (per >> 32) ? (int)(in / per) : (int)((unsigned)in / (unsigned)per);
     const unsigned long long off = in - (unsigned long long)g * per;
     int r0;
     const int m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, nullptr), N = paged_tokens(a.p.kv, b, nullptr);
@@ -718,25 +732,30 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
         float sv[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) sv[x] = __uint_as_float(q[x]);
-        // Halves of blocks that every row of the warp sees whole skip the masks,
-        // and with a positive scale the maximum is taken on raw scores.
-        const bool all = kh0 + 31 <= qpos && (window == 0 || kh0 > qpos - window || kh0 + 32 <= sinks);
-        const bool fast = bad == 0 && sl2 > 0.f && __all_sync(0xffffffffu, !vok || all);
-        float mq[2] = {ninf, ninf}, mul = sl2;
-        if (fast) {
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) mq[(x >> 1) & 1] = max3(mq[(x >> 1) & 1], sv[x], sv[x + 1]);
-        } else {
+        // With a positive scale the maximum is taken on raw scores; any other is
+        // multiplied in first.
+        float mul = sl2;
+        if (!(sl2 > 0.f)) {
           mul = 1.f;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const bool see = row_sees(qpos, kh0 + x, window, sinks) && !((bad >> (2 * half + x / 16)) & 1u);
-            sv[x] = see ? sv[x] * sl2 : ninf;
-            mq[x & 1] = fmaxf(mq[x & 1], sv[x]);
-          }
+          for (int x = 0; x < 32; ++x) sv[x] *= sl2;
         }
-        float mx = fmaxf(mq[0], mq[1]);
-        if (fast) mx *= sl2;
+        // Halves of blocks that every row of the warp sees whole skip the mask.
+        const bool all = kh0 + 31 <= qpos && (window == 0 || kh0 > qpos - window || kh0 + 32 <= sinks);
+        if (bad != 0 || !__all_sync(0xffffffffu, !vok || all)) {
+          // bit x: token kh0 + x is seen
+          uint32_t see = first_bits(qpos - kh0 + 1);
+          if (window) see &= ~first_bits(qpos - window - kh0 + 1) | first_bits(sinks - kh0);
+          const uint32_t b2 = bad >> (2 * half);
+          see &= ~((b2 & 1u ? 0x0000ffffu : 0u) | (b2 & 2u ? 0xffff0000u : 0u));
+#pragma unroll
+          for (int x = 0; x < 32; ++x) sv[x] = (see >> x) & 1u ? sv[x] : ninf;
+        }
+        float mq[2] = {ninf, ninf};
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) mq[(x >> 1) & 1] = max3(mq[(x >> 1) & 1], sv[x], sv[x + 1]);
+        const float mx1 = fmaxf(mq[0], mq[1]);
+        float mx = mx1 == ninf ? ninf : mx1 * mul;
         if (pair_any(id, mx > mref + 8.f || (mref == ninf && mx > ninf))) {
           // rare: the row's maximum over both halves, and what follows from it
           if (half == 0) *xr = mx;
@@ -914,12 +933,8 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
       }
       tc::fence_before_sync();
       if (tid == 0 && !whole && sg.i0 == 0) {
-        // the CTA that holds the pair's last block
-        const unsigned long long nc = s_plan.n_cta, total = s_plan.total, x = sg.w + sg.cost - 1;
-        unsigned long long c = x * nc / total;
-        while (c + 1 < nc && total * (c + 1) / nc <= x) ++c;
-        while (c > 0 && total * c / nc > x) --c;
-        a.recs[blockIdx.x] = ChunkRec{sg.row0, sg.rows, sg.g, (int)c, sg.single ? 1 : 0};
+        const int c = s_plan.cta_of(sg.w + sg.cost - 1);  // it holds the pair's last block
+        a.recs[blockIdx.x] = ChunkRec{sg.row0, sg.rows, sg.g, c, sg.single ? 1 : 0};
       }
     }
   }

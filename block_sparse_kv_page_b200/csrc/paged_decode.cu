@@ -173,13 +173,16 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
     ex = prefix(w, t) + total;
     total += t;
   }
-  const long long most = total / kMinShare;
-  const int nc = (int)(most < 1 ? 1 : (most < (long long)gridDim.x ? most : (long long)gridDim.x));
+  // as many CTAs as have kMinShare each; the first `more` of them take one tile more than `each`
+  const int nc = total >= (long long)gridDim.x * kMinShare ? (int)gridDim.x : max(1, (int)total / kMinShare);
+  const long long each = total >> 31 ? total / nc : (int)total / nc;
+  const int more = (int)(total - each * nc);
   if ((int)blockIdx.x >= nc) {
     if (!a.by_unit && tid == 0) a.recs[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const long long w0 = total * blockIdx.x / nc, w1 = total * (blockIdx.x + 1) / nc;
+  const long long w0 = each * blockIdx.x + min((int)blockIdx.x, more);
+  const long long w1 = w0 + each + ((int)blockIdx.x < more ? 1 : 0);
   {
     long long run = 0;
     for (int b0 = 0; b0 < B; b0 += kThreads) {
@@ -198,7 +201,9 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
   __syncthreads();
   int b = (int)s_plan[1];
   Unit u = unit_of(a, b, nullptr);
-  int g = (int)(s_plan[0] / (u.nt + kC0)), off = (int)(s_plan[0] % (u.nt + kC0));
+  const long long in = s_plan[0];  // into the sequence's work
+  int g = in >> 31 ? (int)(in / (u.nt + kC0)) : (int)in / (u.nt + kC0);
+  int off = (int)(in - (long long)g * (u.nt + kC0));
   long long rem = w1 - w0, at = w0 - off;  // at: where the unit's work begins
   if (!a.by_unit && tid == 0) a.recs[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
@@ -628,11 +633,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       if (tid == 0 && i0 == 0) {  // whether, and up to which CTA, the unit goes on
         int last = -1;
         if (!whole) {
-          const long long x = at + cost - 1;
-          long long l = x * nc / total;
-          while (l + 1 < nc && total * (l + 1) / nc <= x) ++l;
-          while (l > 0 && total * l / nc > x) --l;
-          last = (int)l;
+          const long long x = at + cost - 1, longer = (each + 1) * more;
+          last = x < longer ? (int)(x / (each + 1)) : (int)(more + (x - longer) / each);
         }
         if (a.by_unit) a.recs[b * Hkv + g] = make_int4(last < 0 ? -1 : (int)blockIdx.x, last, b, g);
         else if (last >= 0) a.recs[blockIdx.x] = make_int4((int)blockIdx.x, last, b, g);
