@@ -52,8 +52,8 @@ PagedScratch paged_scratch() {
   const size_t sms = (size_t)device_sm_count();
   PagedScratch s;
   s.parts = kScratch;
-  s.xbuf = s.parts + align256(sms * 2 * 2 * 128 * kChunkPart * sizeof(float));
-  s.recs = s.xbuf + align256(sms * 128 * kChunkPart * sizeof(float));
+  s.xbuf = s.parts + align256(sms * 2 * 2 * kChunkPart * sizeof(float));
+  s.recs = s.xbuf + align256(sms * kChunkPart * sizeof(float));
   s.total = s.recs + align256(sms * sizeof(ChunkRec));
   // (the decode's parts and records, smaller, lie in the same place)
   return s;

@@ -856,25 +856,25 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
       const bool merge = sg.single && sg.nb > 0;  // both slots have a part of the rows
       float f0 = 1.f, f1 = 0.f;                   // weights of this slot's and the other slot's result
       const float* other = nullptr;
-      float* xrow = a.xbuf + ((size_t)blockIdx.x * 128 + r) * kChunkPart;
+      float* xpart = a.xbuf + (size_t)blockIdx.x * kChunkPart;
       if (merge && t == 1 && nx > 0) wait(x_empty, (nx - 1) & 1u);
       if (merge && t == 0) {
         wait(x_full, nx & 1u);
-        const float m1 = __ldcg(xrow + kHeadDim), l1 = __ldcg(xrow + kHeadDim + 1);
-        const float M = fmaxf(mref, m1);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(xpart + kChunkMl + 2 * r));
+        const float M = fmaxf(mref, ml.x);
         if (M != ninf) {
           f0 = fast_exp2(mref - M);
-          f1 = fast_exp2(m1 - M);
+          f1 = fast_exp2(ml.x - M);
         }
-        lh = lh * f0 + l1 * f1;
+        lh = lh * f0 + ml.y * f1;
         mref = M;
-        other = xrow;
+        other = xpart;
       }
       float* part = nullptr;  // where an unnormalised result goes
       if (merge && t == 1) {
-        part = xrow;
+        part = xpart;
       } else if (!whole) {
-        part = a.parts + ((((size_t)blockIdx.x * 2 + (sg.i0 == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart;
+        part = a.parts + (((size_t)blockIdx.x * 2 + (sg.i0 == 0 ? 1 : 0)) * 2 + t) * kChunkPart;
       }
       const float inv = part ? 1.f : (lh > 0.f ? 1.f / lh : 0.f);
       const size_t orow = vok ? (size_t)(sg.row0 + row) * a.p.Hq + (size_t)sg.g * G + hh : 0;
@@ -896,19 +896,27 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
 #pragma unroll
         for (int x = 0; x < 16; ++x) o[x] = __uint_as_float(q[x]) * f0;
         const int d0 = 64 * half + 16 * c;
+        // (parts lie by groups of 4 dims, rows within: a warp's accesses are whole lines)
         if (other) {
+          float4 y[4];
 #pragma unroll
-          for (int x = 0; x < 16; x += 4) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(other + d0 + x));
-            o[x] += y.x * f1;
-            o[x + 1] += y.y * f1;
-            o[x + 2] += y.z * f1;
-            o[x + 3] += y.w * f1;
+          for (int x = 0; x < 4; ++x) y[x] = __ldcg(reinterpret_cast<const float4*>(other) + (d0 / 4 + x) * 128 + r);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            o[4 * x] += y[x].x * f1;
+            o[4 * x + 1] += y[x].y * f1;
+            o[4 * x + 2] += y[x].z * f1;
+            o[4 * x + 3] += y[x].w * f1;
           }
         }
         if (mine) {
-          if (part || a.p.out) {
-            float* d = (part ? part : a.p.out + orow * kHeadDim) + d0;
+          if (part) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              reinterpret_cast<float4*>(part)[(d0 / 4 + x) * 128 + r] =
+                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          } else if (a.p.out) {
+            float* d = a.p.out + orow * kHeadDim + d0;
 #pragma unroll
             for (int x = 0; x < 16; x += 4)
               *reinterpret_cast<float4*>(d + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
@@ -921,7 +929,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
         }
       }
       if (mine && half == 0) {
-        if (part) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mref, lh);
+        if (part) *reinterpret_cast<float2*>(part + kChunkMl + 2 * r) = make_float2(mref, lh);
         else if (a.p.lse) a.p.lse[orow] = lh > 0.f ? mref * kLn2 + logf(lh) : ninf;
         if (sg.i0 == 0 && qpos < 0) flag_status(status, SA_ERR_DEVICE_CHECK);
       }
@@ -944,38 +952,43 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
-// Merge of the partial results of the pairs that were cut: a task is eight
-// vectors of the pair that one CTA began, a warp takes one of them, lane l its
-// dims 4 l .. 4 l + 3; parts in CTA order.  Tasks go round the grid, so that the
-// few pairs of a short chunk over a long cache (many parts each) use every SM.
+// Merge of the partial results of the pairs that were cut: a warp's task is 32
+// vectors (one per lane) and 8 dims of the pair that one CTA began, its parts in
+// CTA order.  Tasks go round the grid, so that the few pairs of a short chunk
+// over a long cache, in many parts each, use every SM.
 constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ ChunkArgs a, int ctas) {
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float ninf = -__int_as_float(0x7f800000);
   const int G = a.p.G, R = a.R;
-  for (int task = blockIdx.x; task < ctas * 32; task += gridDim.x) {
-    const int c0 = task >> 5;
+  const int stride = gridDim.x * (kCombineThreads / 32);
+  for (int task = warp * gridDim.x + blockIdx.x; task < ctas * 128; task += stride) {
+    const int c0 = task >> 7;
     const ChunkRec rec = a.recs[c0];
     if (rec.rows <= 0) continue;
-    const int v = (task & 31) * 8 + warp;
+    const int v = ((task >> 4) & 7) * 32 + lane, d4 = (task & 15) * 2;  // vector; group of 4 dims
     const int t = v >> 7, r = v & 127;
     const int rr = r / G, row = t * R + rr;
-    if (r >= G * R || row >= rec.rows || (rec.single && t)) continue;
+    if (rec.single && t) continue;
+    const bool ok = r < G * R && row < rec.rows;
+    if (!__any_sync(0xffffffffu, ok)) continue;
     float M = ninf, L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     const int np = rec.last - c0 + 1;
-    constexpr int kBatch = 16;
+    constexpr int kBatch = 8;
     for (int p0 = 0; p0 < np; p0 += kBatch) {
       float2 ml[kBatch];
-      float4 y[kBatch];
+      float4 y[kBatch][2];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int p = p0 + i;
-        const bool ok = p < np;
-        const float* src = a.parts + ((((size_t)(c0 + (ok ? p : 0)) * 2 + (!ok || p == 0 ? 1 : 0)) * 2 + t) * 128 + r) * kChunkPart;
-        ml[i] = ok ? __ldcg(reinterpret_cast<const float2*>(src + kHeadDim)) : make_float2(ninf, 0.f);
-        y[i] = ok ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool in = p < np && ok;
+        const float* src = a.parts + (((size_t)(c0 + (in ? p : 0)) * 2 + (!in || p == 0 ? 1 : 0)) * 2 + t) * kChunkPart;
+        ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(src + kChunkMl + 2 * r)) : make_float2(ninf, 0.f);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          y[i][x] = in ? __ldcg(reinterpret_cast<const float4*>(src) + (d4 + x) * 128 + r) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float nm = M;
 #pragma unroll
@@ -983,26 +996,36 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
       if (nm == ninf) continue;
       const float f = fast_exp2(M - nm);
       L *= f;
-      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const float w = fast_exp2(ml[i].x - nm);
         L += ml[i].y * w;
-        o.x += y[i].x * w;
-        o.y += y[i].y * w;
-        o.z += y[i].z * w;
-        o.w += y[i].w * w;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          o[x].x += y[i][x].x * w;
+          o[x].y += y[i][x].y * w;
+          o[x].z += y[i][x].z * w;
+          o[x].w += y[i][x].w * w;
+        }
       }
       M = nm;
     }
+    if (!ok) continue;
     const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) o[x] = make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
     const size_t orow = (size_t)(rec.row0 + row) * a.p.Hq + (size_t)rec.g * G + (r - rr * G);
-    if (a.p.out)
-      *reinterpret_cast<float4*>(a.p.out + orow * kHeadDim + 4 * lane) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    else
-      *reinterpret_cast<uint2*>(a.p.out_bf16 + orow * kHeadDim + 4 * lane) =
-          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (a.p.lse && lane == 0) a.p.lse[orow] = L > 0.f ? M * kLn2 + logf(L) : ninf;
+    if (a.p.out) {
+      float4* d = reinterpret_cast<float4*>(a.p.out + orow * kHeadDim) + d4;
+      d[0] = o[0];
+      d[1] = o[1];
+    } else {
+      *reinterpret_cast<uint4*>(a.p.out_bf16 + orow * kHeadDim + 4 * d4) =
+          make_uint4(pack_bf16(o[0].x, o[0].y), pack_bf16(o[0].z, o[0].w), pack_bf16(o[1].x, o[1].y), pack_bf16(o[1].z, o[1].w));
+    }
+    if (a.p.lse && d4 == 0) a.p.lse[orow] = L > 0.f ? M * kLn2 + logf(L) : ninf;
   }
 }
 

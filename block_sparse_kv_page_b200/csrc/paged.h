@@ -63,7 +63,9 @@ struct PagedAttnArgs {
 };
 
 // Chunk attention (chunk_attn.cu).
-constexpr int kChunkPart = 128 + 4;  // floats of a partial result: acc[128], reference maximum, sum, 2 unused
+// A partial result of 128 vectors: [32 groups of 4 dims][128 vectors][4], then
+// [128][reference maximum, sum].
+constexpr int kChunkMl = 128 * 128, kChunkPart = kChunkMl + 2 * 128;
 struct ChunkRec {                    // a pair cut between CTAs, kept by the CTA that holds its first block
   int row0, rows, g, last, single;   // rows 0: none; last: the CTA that holds its last block
 };
@@ -75,8 +77,8 @@ struct ChunkArgs {
   float scale_log2;                  // scale * log2(e)
   int R;                             // rows of a tile, floor(128 / G)
   int hb;                            // rows of a K or V box: divides page_size and the block
-  float* parts;                      // [grid][head, tail segment][slot][128][kChunkPart]
-  float* xbuf;                       // [grid][128][kChunkPart]
+  float* parts;                      // [grid][head, tail segment][slot][kChunkPart]
+  float* xbuf;                       // [grid][kChunkPart]
   ChunkRec* recs;                    // [grid]
 };
 cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st);
