@@ -11,58 +11,59 @@ namespace {
 
 constexpr int kWriteThreads = 256;
 
-// Write: 16 lanes share one (row, head), 8 values of its K and of its V each:
-// one 16-byte load per lane and row, the maximum by four shuffles inside the
-// half warp, one 8-byte (e4m3) or 16-byte (bf16) store.
+// Write: 16 lanes share a row and HG of its heads, 8 values of each K and V row
+// per lane: every load of the heads is issued first, the maximum goes through
+// four shuffles inside the half warp, the stores are 8 bytes (e4m3) or 16 a
+// lane.  The row's place (its sequence, its page) is found once for the HG
+// heads; with a head at a time, and 64-bit divisions, those instructions bound
+// the kernel (219 us for eight prompts, 947 MB).
 template <bool E4M3>
-SA_DEV void write_row(const CacheWriteArgs& a, const uint4 x, unsigned char* pool, uint8_t* scale, long long off,
-                      size_t at, int l) {
+SA_DEV void write_row(const uint4 x, unsigned char* dst, uint8_t* scale, int l, bool ok) {
   if (!E4M3) {
-    *reinterpret_cast<uint4*>(pool + off + 16 * l) = x;
+    if (ok) *reinterpret_cast<uint4*>(dst + 16 * l) = x;
     return;
   }
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float f[8], m = 0.f;
+  // |bf16| compare as their bits do
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-    m = fmaxf(m, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-  }
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int k = e4m3_exponent(m);
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int k = e4m3_exponent(__uint_as_float(m << 16));
   const float inv = __uint_as_float((uint32_t)(127 - k) << 23);  // 2^-k: the product is exact
   uint32_t c[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE,
-                                                 __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv),
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[2 * i]) * inv, bf16_hi(w[2 * i]) * inv),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[2 * i + 1]) * inv, bf16_hi(w[2 * i + 1]) * inv),
                                                  __NV_SATFINITE, __NV_E4M3);
     c[i] = lo | (hi << 16);
   }
-  if (off >= 0) {
-    *reinterpret_cast<uint2*>(pool + off + 8 * l) = make_uint2(c[0], c[1]);
-    if (l == 0) scale[at] = (uint8_t)(k + 127);
+  if (ok) {
+    *reinterpret_cast<uint2*>(dst + 8 * l) = make_uint2(c[0], c[1]);
+    if (l == 0) *scale = (uint8_t)(k + 127);
   }
 }
 
-template <bool E4M3>
+template <bool E4M3, int HG>
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
   const int l = threadIdx.x & 15;
-  const long long x = ((long long)blockIdx.x * kWriteThreads + threadIdx.x) >> 4;  // (row, head)
-  const long long all = (long long)a.n_rows * a.kv.Hkv;
-  const int Hkv = a.kv.Hkv;
-  const int row = (int)(x / Hkv), h = (int)(x % Hkv);
-  // the row's sequence: the last b with row_off[b] <= row (empty ones skipped)
-  long long off = -1;
-  size_t at = 0;
-  uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
-  if (x < all) {
-    const size_t src = (size_t)row * a.row_stride + (size_t)h * kHeadDim + 8 * l;
-    kx = ldg_nc128(a.k_new + src);
-    vx = ldg_nc128(a.v_new + src);
+  const unsigned groups = (unsigned)a.kv.Hkv / HG;
+  const unsigned x = blockIdx.x * (kWriteThreads / 16) + (threadIdx.x >> 4);  // (row, group of heads)
+  const int row = (int)(x / groups), h0 = (int)(x - (unsigned)row * groups) * HG;
+  const bool in = row < a.n_rows;
+  uint4 kx[HG], vx[HG];
+  const size_t src = (size_t)row * a.row_stride + (size_t)h0 * kHeadDim + 8 * l;
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    kx[h] = in ? ldg_nc128(a.k_new + src + h * kHeadDim) : make_uint4(0u, 0u, 0u, 0u);
+    vx[h] = in ? ldg_nc128(a.v_new + src + h * kHeadDim) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  int page = -1, slot = 0;
+  if (in) {
+    // the row's sequence: the last b with row_off[b] <= row (empty ones skipped)
     int lo = 0, hi = a.kv.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -77,18 +78,21 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
       if (t < 0) {
         flag_status(a.status, SA_ERR_DEVICE_CHECK);
       } else {
-        const int p = t / a.kv.page_size, slot = t - p * a.kv.page_size;
-        const int page = paged_page(a.kv, lo, p, a.status);
-        if (page >= 0) {
-          off = paged_offset(a.kv, page, h, slot);
-          at = scale_index(a.kv, page, h, slot);
-        }
+        const int p = t / a.kv.page_size;
+        slot = t - p * a.kv.page_size;
+        page = paged_page(a.kv, lo, p, a.status);
       }
     }
   }
-  if (E4M3 || off >= 0) {
-    write_row<E4M3>(a, kx, a.kv.k, a.kv.k_scale, off, at, l);
-    write_row<E4M3>(a, vx, a.kv.v, a.kv.v_scale, off, at, l);
+  const bool ok = page >= 0;
+  const long long off = paged_offset(a.kv, ok ? page : 0, h0, slot);
+  const size_t at = scale_index(a.kv, ok ? page : 0, h0, slot);
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    const long long o = off + h * a.kv.head_stride;
+    const size_t s = at + (size_t)h * a.kv.page_size;
+    write_row<E4M3>(kx[h], a.kv.k + o, a.kv.k_scale + s, l, ok);
+    write_row<E4M3>(vx[h], a.kv.v + o, a.kv.v_scale + s, l, ok);
   }
 }
 
@@ -100,81 +104,94 @@ SA_DEV uint32_t bf16_pair_of_codes(uint32_t two, float scale) {
   return pack_bf16(f.x * scale, f.y * scale);  // exact
 }
 
-// Read: a warp takes 16 tokens of one (sequence, head), 4 rows at a time.
+// Read: a warp takes 16 tokens of one (sequence, head): all of its loads first
+// (8 lanes per row of codes, 16 per bf16 row), then the stores.
 template <bool E4M3>
-__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ CacheReadArgs a, int tiles) {
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ CacheReadArgs a, unsigned tiles) {
   const int lane = threadIdx.x & 31;
-  const long long warp = ((long long)blockIdx.x * kReadThreads + threadIdx.x) >> 5;
-  const long long warps = (long long)gridDim.x * (kReadThreads / 32);
-  const long long items = (long long)a.kv.B * a.kv.Hkv * tiles;
-  for (long long it = warp; it < items; it += warps) {
-    const int tile = (int)(it % tiles);
-    const int u = (int)(it / tiles);
-    const int b = u / a.kv.Hkv, h = u % a.kv.Hkv;
+  const unsigned warps = gridDim.x * (kReadThreads / 32);
+  const unsigned heads = (unsigned)a.kv.Hkv;
+  for (unsigned it = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5); it < a.items; it += warps) {
+    const unsigned u = it / tiles, tile = it - u * tiles;
+    const int b = (int)(u / heads), h = (int)(u - (unsigned)b * heads), t0 = (int)tile * 16;
     const int N = paged_tokens(a.kv, b, a.status);
-    const int t0 = a.first_token >= 0 ? a.first_token : max(0, N + a.first_token);
-    int e = min(N, tile * 16 + 16);
-    const int s = max(t0, tile * 16);
+    const int first = a.first_token >= 0 ? a.first_token : max(0, N + a.first_token);
+    int e = min(N, t0 + 16);
+    const int s = max(first, t0);
     if (s >= e) continue;
     if (e > a.cap) {
       flag_status(a.status, SA_ERR_DEVICE_CHECK);
       e = (int)a.cap;
       if (s >= e) continue;
     }
-    const int p = tile * 16 / a.kv.page_size;
+    const int p = t0 / a.kv.page_size;
     const int page = paged_page(a.kv, b, p, a.status);
     if (page < 0) continue;
-    const int slot0 = tile * 16 - p * a.kv.page_size;
+    const int slot0 = t0 - p * a.kv.page_size;
     const long long off = paged_offset(a.kv, page, h, slot0);
     const size_t at = scale_index(a.kv, page, h, slot0);
-    const size_t dst = ((size_t)u * a.cap + (size_t)tile * 16) * kHeadDim;
-    const int r4 = lane >> 3, l = lane & 7;
+    const size_t dst = ((size_t)u * a.cap + (size_t)t0) * kHeadDim;
+    constexpr int kLanes = E4M3 ? 8 : 16, kRows = 32 / kLanes, kIter = 16 / kRows;  // lanes of a row, rows at a time
+    const int rl = lane / kLanes, l = lane % kLanes;
+    uint4 x[2][kIter];
+    uint32_t sc[2][kIter];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const unsigned char* src = (kv ? a.kv.v : a.kv.k) + off;
-      __nv_bfloat16* out = (kv ? a.v_out : a.k_out) + dst;
+    for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * i + r4;
-        const int t = tile * 16 + r;
+      for (int i = 0; i < kIter; ++i) {
+        const int r = kRows * i + rl, t = t0 + r;
+        const bool in = t >= s && t < e;
+        x[kv][i] = in ? ldg_nc128((kv ? a.kv.v : a.kv.k) + off + r * a.kv.token_stride + 16 * l) : make_uint4(0u, 0u, 0u, 0u);
+        sc[kv][i] = E4M3 && in ? __ldg((kv ? a.kv.v_scale : a.kv.k_scale) + at + r) : 0u;
+      }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int r = kRows * i + rl, t = t0 + r;
         if (t < s || t >= e) continue;
-        uint4* o = reinterpret_cast<uint4*>(out + r * kHeadDim + 16 * l);
+        uint4* o = reinterpret_cast<uint4*>((kv ? a.v_out : a.k_out) + dst + r * kHeadDim + (E4M3 ? 16 : 8) * l);
+        const uint4 c = x[kv][i];
         if (E4M3) {
-          const uint4 c = ldg_nc128(src + r * a.kv.token_stride + 16 * l);
-          const float sc = __uint_as_float((uint32_t)__ldg((kv ? a.kv.v_scale : a.kv.k_scale) + at + r) << 23);
-          o[0] = make_uint4(bf16_pair_of_codes(c.x & 0xffffu, sc), bf16_pair_of_codes(c.x >> 16, sc),
-                            bf16_pair_of_codes(c.y & 0xffffu, sc), bf16_pair_of_codes(c.y >> 16, sc));
-          o[1] = make_uint4(bf16_pair_of_codes(c.z & 0xffffu, sc), bf16_pair_of_codes(c.z >> 16, sc),
-                            bf16_pair_of_codes(c.w & 0xffffu, sc), bf16_pair_of_codes(c.w >> 16, sc));
+          const float f = __uint_as_float(sc[kv][i] << 23);
+          o[0] = make_uint4(bf16_pair_of_codes(c.x & 0xffffu, f), bf16_pair_of_codes(c.x >> 16, f),
+                            bf16_pair_of_codes(c.y & 0xffffu, f), bf16_pair_of_codes(c.y >> 16, f));
+          o[1] = make_uint4(bf16_pair_of_codes(c.z & 0xffffu, f), bf16_pair_of_codes(c.z >> 16, f),
+                            bf16_pair_of_codes(c.w & 0xffffu, f), bf16_pair_of_codes(c.w >> 16, f));
         } else {
-          const unsigned char* r_src = src + r * a.kv.token_stride + 32 * l;
-          o[0] = ldg_nc128(r_src);
-          o[1] = ldg_nc128(r_src + 16);
+          o[0] = c;
         }
       }
-    }
   }
+}
+
+template <bool E4M3>
+cudaError_t launch_write(const CacheWriteArgs& a, cudaStream_t st) {
+  const int hg = a.kv.Hkv % 4 == 0 ? 4 : (a.kv.Hkv % 2 == 0 ? 2 : 1);
+  const long long threads = (long long)a.n_rows * (a.kv.Hkv / hg) * 16;
+  const unsigned blocks = (unsigned)((threads + kWriteThreads - 1) / kWriteThreads);
+  if (hg == 4) cache_write_kernel<E4M3, 4><<<blocks, kWriteThreads, 0, st>>>(a);
+  else if (hg == 2) cache_write_kernel<E4M3, 2><<<blocks, kWriteThreads, 0, st>>>(a);
+  else cache_write_kernel<E4M3, 1><<<blocks, kWriteThreads, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t st) {
-  const long long threads = (long long)a.n_rows * a.kv.Hkv * 16;
-  const long long blocks = (threads + kWriteThreads - 1) / kWriteThreads;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (a.kv.e4m3) cache_write_kernel<true><<<(unsigned)blocks, kWriteThreads, 0, st>>>(a);
-  else cache_write_kernel<false><<<(unsigned)blocks, kWriteThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return a.kv.e4m3 ? launch_write<true>(a, st) : launch_write<false>(a, st);
 }
 
-cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t st) {
-  const int tiles = (int)((long long)a.kv.max_pages * a.kv.page_size / 16);
+cudaError_t launch_cache_read(CacheReadArgs a, cudaStream_t st) {
+  const long long tiles = (long long)a.kv.max_pages * a.kv.page_size / 16;
   const long long items = (long long)a.kv.B * a.kv.Hkv * tiles;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  a.items = (unsigned)items;
   const long long per = kReadThreads / 32;
   long long blocks = (items + per - 1) / per;
   if (blocks > 148 * 16) blocks = 148 * 16;
-  if (a.kv.e4m3) cache_read_kernel<true><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, tiles);
-  else cache_read_kernel<false><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, tiles);
+  if (a.kv.e4m3) cache_read_kernel<true><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, (unsigned)tiles);
+  else cache_read_kernel<false><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, (unsigned)tiles);
   return cudaGetLastError();
 }
 

@@ -43,9 +43,10 @@ struct CacheReadArgs {
   __nv_bfloat16* k_out;        // [B][Hkv][cap][128]
   __nv_bfloat16* v_out;
   long long cap;
+  unsigned items;              // (sequence, head, 16 tokens) triples
   int* status;                 // nullable
 };
-cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t st);
+cudaError_t launch_cache_read(CacheReadArgs a, cudaStream_t st);
 
 struct PagedAttnArgs {
   PagedView kv;
