@@ -261,7 +261,7 @@ sa_status sparse_attn_cache_read(const sa_paged_desc* kv, int32_t first_token, v
   if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || cap_tokens < 1) return SA_ERR_INVALID;
   if ((s = status_word(ws, ws_bytes, &a.status)) != SA_OK) return s;
   // one item per (sequence, head, 16 tokens)
-  if ((double)kv->batch * kv->n_kv_heads * kv->max_pages * (kv->page_size / 16) > 2147483647.0)
+  if ((double)kv->batch * kv->n_kv_heads * kv->max_pages * (kv->page_size / 16) > 1073741823.0)
     return SA_ERR_UNSUPPORTED;
   a.kv = paged_view(kv);
   a.first_token = first_token;

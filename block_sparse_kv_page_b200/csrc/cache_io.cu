@@ -104,14 +104,16 @@ SA_DEV uint32_t bf16_pair_of_codes(uint32_t two, float scale) {
   return pack_bf16(f.x * scale, f.y * scale);  // exact
 }
 
-// Read: a warp takes 16 tokens of one (sequence, head): all of its loads first
-// (8 lanes per row of codes, 16 per bf16 row), then the stores.
+// Read: a warp takes the K or the V of 16 tokens of one (sequence, head), 16
+// lanes a row, so that every store instruction writes whole rows; its loads come
+// first, all at once.
 template <bool E4M3>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ CacheReadArgs a, unsigned tiles) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, rl = lane >> 4, l = lane & 15;
   const unsigned warps = gridDim.x * (kReadThreads / 32);
   const unsigned heads = (unsigned)a.kv.Hkv;
-  for (unsigned it = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5); it < a.items; it += warps) {
+  for (unsigned x = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5); x < 2 * a.items; x += warps) {
+    const unsigned it = x >> 1;
     const unsigned u = it / tiles, tile = it - u * tiles;
     const int b = (int)(u / heads), h = (int)(u - (unsigned)b * heads), t0 = (int)tile * 16;
     const int N = paged_tokens(a.kv, b, a.status);
@@ -128,40 +130,40 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
     const int page = paged_page(a.kv, b, p, a.status);
     if (page < 0) continue;
     const int slot0 = t0 - p * a.kv.page_size;
-    const long long off = paged_offset(a.kv, page, h, slot0);
-    const size_t at = scale_index(a.kv, page, h, slot0);
-    const size_t dst = ((size_t)u * a.cap + (size_t)t0) * kHeadDim;
-    constexpr int kLanes = E4M3 ? 8 : 16, kRows = 32 / kLanes, kIter = 16 / kRows;  // lanes of a row, rows at a time
-    const int rl = lane / kLanes, l = lane % kLanes;
-    uint4 x[2][kIter];
-    uint32_t sc[2][kIter];
+    const unsigned char* src = ((x & 1) ? a.kv.v : a.kv.k) + paged_offset(a.kv, page, h, slot0) +
+                               rl * a.kv.token_stride + (E4M3 ? 8 : 16) * l;
+    const uint8_t* scale = E4M3 ? ((x & 1) ? a.kv.v_scale : a.kv.k_scale) + scale_index(a.kv, page, h, slot0) + rl : nullptr;
+    __nv_bfloat16* dst = ((x & 1) ? a.v_out : a.k_out) + ((size_t)u * a.cap + (size_t)(t0 + rl)) * kHeadDim + 8 * l;
+    uint4 v[8];
+    uint32_t sc[8];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int r = kRows * i + rl, t = t0 + r;
-        const bool in = t >= s && t < e;
-        x[kv][i] = in ? ldg_nc128((kv ? a.kv.v : a.kv.k) + off + r * a.kv.token_stride + 16 * l) : make_uint4(0u, 0u, 0u, 0u);
-        sc[kv][i] = E4M3 && in ? __ldg((kv ? a.kv.v_scale : a.kv.k_scale) + at + r) : 0u;
-      }
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int r = kRows * i + rl, t = t0 + r;
-        if (t < s || t >= e) continue;
-        uint4* o = reinterpret_cast<uint4*>((kv ? a.v_out : a.k_out) + dst + r * kHeadDim + (E4M3 ? 16 : 8) * l);
-        const uint4 c = x[kv][i];
-        if (E4M3) {
-          const float f = __uint_as_float(sc[kv][i] << 23);
-          o[0] = make_uint4(bf16_pair_of_codes(c.x & 0xffffu, f), bf16_pair_of_codes(c.x >> 16, f),
-                            bf16_pair_of_codes(c.y & 0xffffu, f), bf16_pair_of_codes(c.y >> 16, f));
-          o[1] = make_uint4(bf16_pair_of_codes(c.z & 0xffffu, f), bf16_pair_of_codes(c.z >> 16, f),
-                            bf16_pair_of_codes(c.w & 0xffffu, f), bf16_pair_of_codes(c.w >> 16, f));
-        } else {
-          o[0] = c;
+    for (int i = 0; i < 8; ++i) {  // rows 2 i + rl
+      const int t = t0 + 2 * i + rl;
+      const bool in = t >= s && t < e;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      sc[i] = 0u;
+      if (E4M3) {
+        if (in) {
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(src + 2 * i * a.kv.token_stride));
+          v[i].x = c.x;
+          v[i].y = c.y;
+          sc[i] = __ldg(scale + 2 * i);
         }
+      } else if (in) {
+        v[i] = ldg_nc128(src + 2 * i * a.kv.token_stride);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = t0 + 2 * i + rl;
+      if (t < s || t >= e) continue;
+      if (E4M3) {
+        const float f = __uint_as_float(sc[i] << 23);
+        v[i] = make_uint4(bf16_pair_of_codes(v[i].x & 0xffffu, f), bf16_pair_of_codes(v[i].x >> 16, f),
+                          bf16_pair_of_codes(v[i].y & 0xffffu, f), bf16_pair_of_codes(v[i].y >> 16, f));
+      }
+      *reinterpret_cast<uint4*>(dst + 2 * i * kHeadDim) = v[i];
+    }
   }
 }
 
@@ -185,10 +187,10 @@ cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t st) {
 cudaError_t launch_cache_read(CacheReadArgs a, cudaStream_t st) {
   const long long tiles = (long long)a.kv.max_pages * a.kv.page_size / 16;
   const long long items = (long long)a.kv.B * a.kv.Hkv * tiles;
-  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (items > 0x3fffffffLL) return cudaErrorInvalidValue;
   a.items = (unsigned)items;
   const long long per = kReadThreads / 32;
-  long long blocks = (items + per - 1) / per;
+  long long blocks = (2 * items + per - 1) / per;
   if (blocks > 148 * 16) blocks = 148 * 16;
   if (a.kv.e4m3) cache_read_kernel<true><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, (unsigned)tiles);
   else cache_read_kernel<false><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, (unsigned)tiles);
