@@ -111,6 +111,16 @@ SA_DEV void reg_fence(uint32_t (&r)[32]) {
                  "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                  "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
+// 16 lanes x 32 fp32 columns: lanes taddr's lane .. + 15 of the warp's quarter;
+// r[4 n .. 4 n + 3] of lane l: row l / 4, columns 8 n + 2 (l % 4) and + 1, then
+// the same columns of row l / 4 + 8.
+SA_DEV void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 SA_DEV void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 // Ties 16 registers filled by ld_32x32b_x16 to this point of the program:
 // placed after wait_ld(), it keeps the compiler from moving their uses above
