@@ -24,9 +24,12 @@
 // CTA, warp-specialised, every wait bounded:
 //   warps 0-7, 8-15  softmax of tile slot 0, 1: two threads per query vector
 //                    (TMEM lane), each half of the block's scores in registers.
-//                    Both use the row's reference maximum, which is only raised
-//                    when a score passes it by 2^8; whether any row needs that
-//                    is one barrier reduction over the pair of warps.  (With a
+//                    Weights are taken against a reference that both threads
+//                    hold; it is raised to the row's maximum only when a half
+//                    block's sum of weights passes 2^20 (fp32 and bf16 hold them
+//                    as exactly there), and the block's weights are taken again;
+//                    whether any row needs that is one barrier reduction over
+//                    the pair of warps, and no maximum is taken otherwise.  (With a
 //                    thread per row, two warps per scheduler, the chain of
 //                    loads, maxima and exponentials was bound by its latency:
 //                    2600 cycles per 64 tokens, 1024 of them exponentials.)
@@ -84,7 +87,7 @@ struct Shape {
   static constexpr int kNumBars = 2 * NS + 2 + 2 * 6 + 2 + 1 + 2 * NR;
   static constexpr int off_bars(bool e4m3) { return kOffRaw + (e4m3 ? NR * kRaw : 0); }
   static constexpr int off_info(bool e4m3) { return off_bars(e4m3) + 8 * kNumBars; }
-  static constexpr int off_scale(bool e4m3) { return (off_info(e4m3) + 4 * kInfo + 15) & ~15; }
+  static constexpr int off_scale(bool e4m3) { return (off_info(e4m3) + 4 * (kInfo + 1) + 15) & ~15; }
   static constexpr int off_x(bool e4m3) { return off_scale(e4m3) + (e4m3 ? NR * BLK : 0); }
   static constexpr int smem(bool e4m3) { return 1024 + off_x(e4m3) + 2 * 128 * 4; }
 };
@@ -370,12 +373,6 @@ SA_DEV unsigned long long add_f2(unsigned long long a, unsigned long long b) {
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-SA_DEV float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 template <bool E4M3, int TERMS>
 __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using Sh = Shape<TERMS>;
@@ -400,6 +397,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
   uint64_t* drain = x_empty + 1;
   uint64_t* raw_full = drain + 1;   // [NR]
   uint64_t* raw_empty = raw_full + NR;
+  // [block % kInfo]: its 16-token pieces on bad pages; [kInfo]: whether any piece ever was
   volatile uint32_t* info = reinterpret_cast<uint32_t*>(base + Sh::off_info(E4M3));
   unsigned char* raw = base + Sh::kOffRaw;
   unsigned char* raw_scale = base + Sh::off_scale(E4M3);  // [NR][BLK]
@@ -428,6 +426,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
     mbar_init(x_full, 8);
     mbar_init(x_empty, 8);
     mbar_init(drain, 3);
+    info[kInfo] = 0u;
     fence_barrier_init();
     prefetch_tmap(&a.tmap_q);
     prefetch_tmap(&a.tmap_k);
@@ -508,7 +507,10 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
             }
             // the softmax reads it once the block's scores are there, which
             // takes this K tile (ordered by the barriers on that way)
-            if (w == 0 && lane == 0) info[n % kInfo] = bad;
+            if (w == 0 && lane == 0) {
+              info[n % kInfo] = bad;
+              if (bad) info[kInfo] = 1u;
+            }
             if (E4M3) {  // codes with their rows' scale bytes
               if (lane == 0) mbar_arrive_expect_tx(raw_full + rs, (uint32_t)Sh::kRaw + boxes * hb);
               __syncwarp();
@@ -717,47 +719,69 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
       const int qpos = vok ? sg.p0 + row : -1;
       float mref = ninf, lh = 0.f;  // reference maximum (log2 units); this half's sum against it
       bool used = false;
+      // Blocks that begin in [plain0, plain0 + plain_n) are seen whole by every
+      // row of the pair.  With a scale that is not positive none counts as such.
+      const int plain0 = window && sg.p1 >= window ? sg.p1 - window + 1 : 0;
+      const unsigned plain_n = sl2 > 0.f ? (unsigned)max(0, sg.p0 + 2 - BLK - plain0) : 0u;
       for (int i = sg.i0; i < sg.i1; ++i, ++n) {
         if (sg.single && (n & 1) != t) continue;
         const int kb0 = (i < sg.sb ? i : sg.wb0 + i - sg.sb) * BLK;
-        const int kh0 = kb0 + 32 * half;  // this thread's first token
         const uint32_t b = cnt % NB, tb = ts + 64u * b;
         wait(s_full + 2 * t + b, (cnt / NB) & 1u);
         tc::fence_after_sync();
         uint32_t q[32];
         tc::ld_32x32b_x32(tb + 32 * half, q);
-        const uint32_t bad = info[n % kInfo];
+        const bool plain = (unsigned)(kb0 - plain0) < plain_n && info[kInfo] == 0u;
         tc::wait_ld();
         tc::reg_fence(q);
-        float sv[32];
+        float sv[32], mul = sl2;
 #pragma unroll
         for (int x = 0; x < 32; ++x) sv[x] = __uint_as_float(q[x]);
-        // With a positive scale the maximum is taken on raw scores; any other is
-        // multiplied in first.
-        float mul = sl2;
-        if (!(sl2 > 0.f)) {
-          mul = 1.f;
-#pragma unroll
-          for (int x = 0; x < 32; ++x) sv[x] *= sl2;
-        }
-        // Halves of blocks that every row of the warp sees whole skip the mask.
-        const bool all = kh0 + 31 <= qpos && (window == 0 || kh0 > qpos - window || kh0 + 32 <= sinks);
-        if (bad != 0 || !__all_sync(0xffffffffu, !vok || all)) {
+        if (!plain) {
+          const uint32_t bad = info[n % kInfo];
           // bit x: token kh0 + x is seen
+          const int kh0 = kb0 + 32 * half;  // this thread's first token
           uint32_t see = first_bits(qpos - kh0 + 1);
           if (window) see &= ~first_bits(qpos - window - kh0 + 1) | first_bits(sinks - kh0);
           const uint32_t b2 = bad >> (2 * half);
           see &= ~((b2 & 1u ? 0x0000ffffu : 0u) | (b2 & 2u ? 0xffff0000u : 0u));
+          mul = 1.f;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) sv[x] = (see >> x) & 1u ? sv[x] : ninf;
+          for (int x = 0; x < 32; ++x) sv[x] = (see >> x) & 1u ? sv[x] * sl2 : ninf;
         }
-        float mq[2] = {ninf, ninf};
+        uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
+        float sum;
+        auto weights = [&] {
+          const float nmn = mref == ninf ? 0.f : -mref;  // nothing seen so far: every p is exp2(-inf) = 0
+          unsigned long long rq[2] = {0ull, 0ull};  // partial sums, two values each
+          const unsigned long long mul2 = pack_f2(mul, mul), nmn2 = pack_f2(nmn, nmn);
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) mq[(x >> 1) & 1] = max3(mq[(x >> 1) & 1], sv[x], sv[x + 1]);
-        const float mx1 = fmaxf(mq[0], mq[1]);
-        float mx = mx1 == ninf ? ninf : mx1 * mul;
-        if (pair_any(id, mx > mref + 8.f || (mref == ninf && mx > ninf))) {
+          for (int j = 0; j < 16; ++j) {
+            float e0, e1;
+            unpack_f2(fma_f2(pack_f2(sv[2 * j], sv[2 * j + 1]), mul2, nmn2), e0, e1);
+            e0 = fast_exp2(e0);
+            e1 = fast_exp2(e1);
+            rq[j & 1] = add_f2(rq[j & 1], pack_f2(e0, e1));
+            p1[j] = pack_bf16(e0, e1);
+            if (TERMS == 3) {
+              const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
+              p2[j] = pack_bf16(d0, d1);
+              p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
+            }
+          }
+          float s0, s1, s2, s3;
+          unpack_f2(rq[0], s0, s1);
+          unpack_f2(rq[1], s2, s3);
+          sum = (s0 + s1) + (s2 + s3);
+        };
+        weights();
+        // (a sum that is NaN because scores are does not ask for it, nor do lanes without a vector)
+        if (pair_any(id, vok && (sum > 0x1p20f || mref == ninf))) {
           // rare: the row's maximum over both halves, and what follows from it
+          float mx = ninf;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) mx = fmaxf(mx, sv[x]);
+          if (mx != ninf) mx *= mul;
           if (half == 0) *xr = mx;
           pair_sync(id);
           if (half == 1) {
@@ -766,7 +790,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
           }
           pair_sync(id);
           if (half == 0) mx = *xr;
-          const bool upd = mx > mref + 8.f || (mref == ninf && mx > ninf);
+          const bool upd = mx > mref;
           const float alpha = !upd ? 1.f : (mref == ninf ? 0.f : fast_exp2(mref - mx));
           if (upd) mref = mx;
           lh *= alpha;
@@ -787,25 +811,9 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
               tc::st_32x32b_x16(to + 16 * c, o);
             }
           }
+          weights();
         }
-        const float nmn = mref == ninf ? 0.f : -mref;  // nothing seen so far: every p is exp2(-inf) = 0
-        unsigned long long rq[2] = {0ull, 0ull};  // partial sums, two values each
-        const unsigned long long mul2 = pack_f2(mul, mul), nmn2 = pack_f2(nmn, nmn);
-        uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float e0, e1;
-          unpack_f2(fma_f2(pack_f2(sv[2 * j], sv[2 * j + 1]), mul2, nmn2), e0, e1);
-          e0 = fast_exp2(e0);
-          e1 = fast_exp2(e1);
-          rq[j & 1] = add_f2(rq[j & 1], pack_f2(e0, e1));
-          p1[j] = pack_bf16(e0, e1);
-          if (TERMS == 3) {
-            const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
-            p2[j] = pack_bf16(d0, d1);
-            p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
-          }
-        }
+        lh += sum;
         // P lies over S: the other half's scores have been read (pair_any)
         tc::st_32x32b_x16(tb + 16 * half, p1);
         if constexpr (TERMS == 3) {
@@ -814,7 +822,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
         }
         // bf16 tiles hold whatever the cache has at tokens that no row of the
         // pair sees: their V rows are zeroed before PV reads them
-        if (!E4M3 && (kb0 + BLK > sg.p1 + 1 || (kb0 < sg.lo && kb0 + BLK > sg.S))) {
+        if (!E4M3 && !plain && (kb0 + BLK > sg.p1 + 1 || (kb0 < sg.lo && kb0 + BLK > sg.S))) {
           const int vs = (2 * n) % NS + 1;
           wait(kv_full + vs, (uint32_t)((2 * n) / NS) & 1u);
           unsigned char* vt = ring + vs * Sh::kSlot;
@@ -829,10 +837,6 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
         tc::fence_before_sync();  // P and the rescaled O before PV reads them
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 2 * t + b);
-        float s0, s1, s2, s3;
-        unpack_f2(rq[0], s0, s1);
-        unpack_f2(rq[1], s2, s3);
-        lh += (s0 + s1) + (s2 + s3);
         ++cnt;
         used = true;
       }
