@@ -729,31 +729,35 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
         const uint32_t b = cnt % NB, tb = ts + 64u * b;
         wait(s_full + 2 * t + b, (cnt / NB) & 1u);
         tc::fence_after_sync();
-        uint32_t q[32];
-        tc::ld_32x32b_x32(tb + 32 * half, q);
         const bool plain = (unsigned)(kb0 - plain0) < plain_n && info[kInfo] == 0u;
-        tc::wait_ld();
-        tc::reg_fence(q);
-        float sv[32], mul = sl2;
+        float sv[32], sum, mul;
+        uint32_t p1[16];
+        auto scores = [&] {
+          {
+            uint32_t q[32];
+            tc::ld_32x32b_x32(tb + 32 * half, q);
+            tc::wait_ld();
+            tc::reg_fence(q);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) sv[x] = __uint_as_float(q[x]);
-        if (!plain) {
-          const uint32_t bad = info[n % kInfo];
-          // bit x: token kh0 + x is seen
-          const int kh0 = kb0 + 32 * half;  // this thread's first token
-          uint32_t see = first_bits(qpos - kh0 + 1);
-          if (window) see &= ~first_bits(qpos - window - kh0 + 1) | first_bits(sinks - kh0);
-          const uint32_t b2 = bad >> (2 * half);
-          see &= ~((b2 & 1u ? 0x0000ffffu : 0u) | (b2 & 2u ? 0xffff0000u : 0u));
-          mul = 1.f;
+            for (int x = 0; x < 32; ++x) sv[x] = __uint_as_float(q[x]);
+          }
+          mul = sl2;
+          if (!plain) {
+            const uint32_t bad = info[n % kInfo];
+            // bit x: token kh0 + x is seen
+            const int kh0 = kb0 + 32 * half;  // this thread's first token
+            uint32_t see = first_bits(qpos - kh0 + 1);
+            if (window) see &= ~first_bits(qpos - window - kh0 + 1) | first_bits(sinks - kh0);
+            const uint32_t b2 = bad >> (2 * half);
+            see &= ~((b2 & 1u ? 0x0000ffffu : 0u) | (b2 & 2u ? 0xffff0000u : 0u));
+            mul = 1.f;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) sv[x] = (see >> x) & 1u ? sv[x] * sl2 : ninf;
-        }
-        uint32_t p1[16], p2[TERMS == 3 ? 16 : 1], p3[TERMS == 3 ? 16 : 1];
-        float sum;
+            for (int x = 0; x < 32; ++x) sv[x] = (see >> x) & 1u ? sv[x] * sl2 : ninf;
+          }
+        };
         auto weights = [&] {
           const float nmn = mref == ninf ? 0.f : -mref;  // nothing seen so far: every p is exp2(-inf) = 0
-          unsigned long long rq[2] = {0ull, 0ull};  // partial sums, two values each
+          unsigned long long rq[2] = {0ull, 0ull};       // partial sums, two values each
           const unsigned long long mul2 = pack_f2(mul, mul), nmn2 = pack_f2(nmn, nmn);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -763,10 +767,9 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
             e1 = fast_exp2(e1);
             rq[j & 1] = add_f2(rq[j & 1], pack_f2(e0, e1));
             p1[j] = pack_bf16(e0, e1);
-            if (TERMS == 3) {
-              const float d0 = e0 - bf16_lo(p1[j]), d1 = e1 - bf16_hi(p1[j]);
-              p2[j] = pack_bf16(d0, d1);
-              p3[j] = pack_bf16(d0 - bf16_lo(p2[j]), d1 - bf16_hi(p2[j]));
+            if (TERMS == 3) {  // what the first term leaves
+              sv[2 * j] = e0 - bf16_lo(p1[j]);
+              sv[2 * j + 1] = e1 - bf16_hi(p1[j]);
             }
           }
           float s0, s1, s2, s3;
@@ -774,9 +777,12 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
           unpack_f2(rq[1], s2, s3);
           sum = (s0 + s1) + (s2 + s3);
         };
+        scores();
         weights();
         // (a sum that is NaN because scores are does not ask for it, nor do lanes without a vector)
         if (pair_any(id, vok && (sum > 0x1p20f || mref == ninf))) {
+          // S is still in place: the scores need not be kept for this
+          scores();
           // rare: the row's maximum over both halves, and what follows from it
           float mx = ninf;
 #pragma unroll
@@ -817,8 +823,16 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
         // P lies over S: the other half's scores have been read (pair_any)
         tc::st_32x32b_x16(tb + 16 * half, p1);
         if constexpr (TERMS == 3) {
-          tc::st_32x32b_x16(tb + 32 + 16 * half, p2);
-          tc::st_32x32b_x16(tb + 64 + 16 * half, p3);
+#pragma unroll
+          for (int x = 1; x < 3; ++x) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              p1[j] = pack_bf16(sv[2 * j], sv[2 * j + 1]);
+              sv[2 * j] -= bf16_lo(p1[j]);
+              sv[2 * j + 1] -= bf16_hi(p1[j]);
+            }
+            tc::st_32x32b_x16(tb + 32 * x + 16 * half, p1);
+          }
         }
         // bf16 tiles hold whatever the cache has at tokens that no row of the
         // pair sees: their V rows are zeroed before PV reads them
