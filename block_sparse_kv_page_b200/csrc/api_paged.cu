@@ -194,7 +194,7 @@ sa_status paged_attention(const sa_paged_desc* kv, const void* q, int64_t q_row_
   if ((s = check_heads(kv, n_q_heads, &a.G)) != SA_OK) return s;
   if (!q || !aligned(q, 16) || q_row_stride < (int64_t)n_q_heads * kHeadDim || q_row_stride % 8)
     return SA_ERR_INVALID;
-  if (n_rows < 0 || window < 0 || sinks < 0 || !std::isfinite(scale)) return SA_ERR_INVALID;
+  if (n_rows < 0 || window < 0 || sinks < 0 || !std::isfinite(scale * kLog2e)) return SA_ERR_INVALID;
   if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return SA_ERR_INVALID;
   if (out_dtype != SA_OUT_F32 && out_dtype != SA_OUT_BF16) return SA_ERR_INVALID;
   const size_t need = sparse_attn_paged_workspace_size(kv, n_q_heads);

@@ -92,6 +92,15 @@ struct Shape {
   static constexpr int smem(bool e4m3) { return 1024 + off_x(e4m3) + 2 * 128 * 4; }
 };
 
+// Registers per thread of the softmax, of the issuing and copying warps and of
+// the converters, once the warpgroups have split what the launch gave them.
+template <bool E4M3>
+struct Regs {
+  static constexpr int kSoftmax = E4M3 ? 88 : 104, kIssue = E4M3 ? 56 : 64, kConvert = 48;
+  static constexpr int kThreads = E4M3 ? 896 : 640;
+  static constexpr int kTotal = 512 * kSoftmax + 128 * kIssue + (E4M3 ? 256 * kConvert : 0);
+};
+
 template <int R>
 SA_DEV void reg_alloc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R));
@@ -374,7 +383,7 @@ SA_DEV unsigned long long add_f2(unsigned long long a, unsigned long long b) {
   return r;
 }
 template <bool E4M3, int TERMS>
-__global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using Sh = Shape<TERMS>;
   constexpr int NS = Sh::NS, NB = Sh::NB;
   extern __shared__ unsigned char smem_raw[];
@@ -448,8 +457,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
   Seg sg;
 
   if (warp >= 16 && warp < 20) {
-    if (E4M3) reg_dealloc<56>();
-    else reg_dealloc<64>();
+    reg_dealloc<Regs<E4M3>::kIssue>();
     if (warp == 16) {
       // ---- producer
       int n = 0, segs = 0, issued = 0;  // issued: K and V tiles
@@ -626,7 +634,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
   } else if (warp >= 20) {
     // ---- e4m3 -> bf16: 8 threads per row, 16 rows at a time
     if constexpr (E4M3) {
-      reg_dealloc<48>();
+      reg_dealloc<Regs<E4M3>::kConvert>();
       const int w = (warp - 20) >> 2;  // K or V
       const int x = (tid - 640) & 127, c = x & 7, r16 = x >> 3;
       int n = 0;
@@ -692,8 +700,7 @@ __global__ void __launch_bounds__(E4M3 ? 896 : 640, 1) chunk_kernel(const __grid
     }
   } else {
     // ---- softmax of slot t, columns 32 half .. 32 half + 31 of a block
-    if (E4M3) reg_alloc<88>();
-    else reg_alloc<104>();
+    reg_alloc<Regs<E4M3>::kSoftmax>();
     const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
     const int id = 1 + 4 * t + quarter;  // barrier of the two warps that share rows
     const int r = 32 * quarter + lane;
@@ -1113,7 +1120,13 @@ cudaError_t launch(const ChunkArgs& a, int grid, cudaStream_t st) {
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   const cudaError_t e = allow_smem((const void*)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, (unsigned)grid, E4M3 ? 896 : 640, smem, st, a);
+  // The split waits for ever if it asks for more than the block was given.
+  static const bool fits = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, (const void*)k) == cudaSuccess && at.numRegs * Regs<E4M3>::kThreads >= Regs<E4M3>::kTotal;
+  }();
+  if (!fits) return cudaErrorInvalidConfiguration;
+  return launch_pdl(k, (unsigned)grid, Regs<E4M3>::kThreads, smem, st, a);
 }
 
 }  // namespace

@@ -457,7 +457,11 @@ def _ws(ws: torch.Tensor | None) -> tuple[int | None, int]:
 
 
 def sparse_attn_paged_workspace_size(kv: PagedCache, n_q_heads: int) -> int:
-    return int(lib.sparse_attn_paged_workspace_size(kv.ref, int(n_q_heads)))
+    """Bytes for the cache's device (they go by its number of SMs)."""
+    if kv.index < 0 or kv.index == torch._C._cuda_getDevice():
+        return int(lib.sparse_attn_paged_workspace_size(kv.ref, int(n_q_heads)))
+    with torch.cuda.device(kv.index):
+        return int(lib.sparse_attn_paged_workspace_size(kv.ref, int(n_q_heads)))
 
 
 def make_paged_workspace(kv: PagedCache, n_q_heads: int, stream=None) -> torch.Tensor:

@@ -422,6 +422,49 @@ def test_large_scores_and_one_hot_rows(cuda_dev, sa, cache, out):
     c.check(c.run(scale=20.0), scale=20.0)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("falling", [False, True])
+def test_scores_that_rise_or_fall_along_the_context(cuda_dev, sa, cache, out, falling):
+    """Keys that are a query times a factor growing (or shrinking) from token to
+    token: the running reference has to follow, for some heads and not others."""
+    for decode in (False, True):
+        c = Case(sa, cuda_dev, lens=[800], rows=[1] if decode else [40], hq=8, hkv=2, page=16, cache=cache, out=out,
+                 seed=125)
+        q = c.q[0, ::4].float()                                    # one query head per KV head
+        for t in range(800):
+            f = (800 - t if falling else t) / 800.0 * 12.0
+            for h in range(2):
+                pg, sl = int(c.table[0, t // 16]), t % 16
+                row = (q[h] * f).to(torch.bfloat16)
+                if c.e4m3:
+                    code, e = PO.quantise_row(row.double().numpy())
+                    c.k.view(torch.uint8)[pg, h, sl] = torch.from_numpy(code)
+                    c.ks[pg, h, sl] = e
+                else:
+                    c.k[pg, h, sl] = row
+        c.dk.view(torch.uint8).copy_(c.k.view(torch.uint8))
+        if c.e4m3:
+            c.dks.copy_(c.ks)
+        for scale in (0.09, 1.0, -0.5):
+            c.check(c.run(decode=decode, scale=scale), scale=scale)
+            c.check(c.run(300, 20, decode=decode, scale=scale), 300, 20, scale=scale)
+        assert c.status() == sa.SA_OK
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("decode", [False, True])
+def test_row_scales_far_apart(cuda_dev, sa, out, decode):
+    """V rows of a cache in e4m3 whose scales differ by up to 2^60, K rows by 2^8."""
+    c = Case(sa, cuda_dev, lens=[900, 70, 33], rows=[1, 1, 1] if decode else [30, 7, 33], hq=8, hkv=2, page=16,
+             cache="e4m3", out=out, seed=126)
+    g = torch.Generator().manual_seed(9)
+    c.vs.copy_(torch.randint(90, 151, c.vs.shape, generator=g, dtype=torch.uint8))
+    c.dvs.copy_(c.vs)
+    c.check(c.run(decode=decode))
+    c.check(c.run(50, 3, decode=decode), 50, 3)
+
+
 def test_offsets_past_32_bits(cuda_dev, sa):
     """Pages 1.5 GiB apart: element and byte offsets pass 2^32."""
     far, n_pages = 3 << 29, 6

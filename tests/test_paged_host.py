@@ -95,6 +95,7 @@ def test_null_cache(lib, abi):
     (dict(sinks=-1), ("chunk", "decode"), "INVALID"),
     (dict(scale=float("nan")), ("chunk", "decode"), "INVALID"),
     (dict(scale=float("inf")), ("chunk", "decode"), "INVALID"),
+    (dict(scale=3e38), ("chunk", "decode"), "INVALID"),   # times log2(e) it is not finite
     (dict(out=None), ("chunk", "decode"), "INVALID"),
     (dict(out=0x400004), ("chunk", "decode"), "INVALID"),
     (dict(dtype=2), ("chunk", "decode"), "INVALID"),
@@ -194,3 +195,11 @@ def test_binding_refuses_bad_rows():
             sa.sparse_attn_paged_decode(c, q, 0.1, 0, 0, out, lse, None)
     with pytest.raises(ValueError):
         sa.sparse_attn_cache_read(c, 0, bf(3, 2, 32, 128), bf(3, 2, 33, 128))
+
+
+def test_workspace_size_through_the_binding():
+    import block_sparse_kv_page_b200 as sa
+    c = _cache()
+    n = sa.sparse_attn_paged_workspace_size(c, 8)
+    assert n > 256 and n % 256 == 0
+    assert sa.sparse_attn_paged_workspace_size(c, 7) == 0
