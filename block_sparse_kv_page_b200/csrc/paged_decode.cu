@@ -103,9 +103,9 @@ SA_DEV uint32_t bf16_low_codes(uint32_t x) {
 struct Unit {
   int N, lo, S, st, wt0, nt;
 };
-SA_DEV Unit unit_of(const PagedDecodeArgs& a, int b, int* status) {
+SA_DEV Unit unit_of(const PagedDecodeArgs& a, int tokens) {
   Unit u;
-  u.N = paged_tokens(a.p.kv, b, status);
+  u.N = tokens;
   u.lo = a.p.window && u.N > a.p.window ? u.N - a.p.window : 0;
   u.S = a.p.window ? min(a.p.sinks, u.N) : 0;
   u.wt0 = u.lo >> 4;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
   using R = Ring<E4M3>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ long long s_scan[kWarps];
-  __shared__ long long s_plan[4];  // total, work in the first sequence before this CTA's, its index, CTAs
+  __shared__ long long s_plan[3];  // work in the first sequence before this CTA's, its index, its tokens
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -165,7 +165,12 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
     total = all;
     return before + x - v;
   };
-  auto seq_work = [&](int b) -> long long { return b < B ? (long long)Hkv * (unit_of(a, b, status).nt + kC0) : 0; };
+  int tokens = 0;  // of the sequence last asked for
+  auto seq_work = [&](int b) -> long long {
+    if (b >= B) return 0;
+    tokens = paged_tokens(kv, b, status);
+    return (long long)Hkv * (unit_of(a, tokens).nt + kC0);
+  };
   long long total = 0, w = 0, ex = 0;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     long long t;
@@ -195,12 +200,13 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       if (w && ex <= w0 && w0 < ex + w) {
         s_plan[0] = w0 - ex;
         s_plan[1] = b0 + tid;
+        s_plan[2] = tokens;
       }
     }
   }
   __syncthreads();
   int b = (int)s_plan[1];
-  Unit u = unit_of(a, b, nullptr);
+  Unit u = unit_of(a, (int)s_plan[2]);
   const long long in = s_plan[0];  // into the sequence's work
   int g = in >> 31 ? (int)(in / (u.nt + kC0)) : (int)in / (u.nt + kC0);
   int off = (int)(in - (long long)g * (u.nt + kC0));
@@ -215,6 +221,30 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
     const int i0 = min(max(off - kC0, 0), u.nt), i1 = min(max(off + take - kC0, 0), u.nt);
     const bool begins = i0 == 0 && (i1 > 0 || (u.nt == 0 && off == 0));
     if (i1 > i0 || begins) {
+      // ---- this warp's tiles, SUB at a time: i0 + SUB (warp + 4 it) + u of
+      // iteration it; lane k keeps the pages of its tiles 32 j + k (in that
+      // order), the next 32 looked up while these are used;
+      // asked for ahead of Q, so that the two latencies overlap
+      const int nt = i1 - i0;
+      const int n_it = max(0, ((nt + SUB - 1) / SUB - warp + kWarps - 1) / kWarps);
+      auto tile_of = [&](int x) { return SUB * (warp + kWarps * (x / SUB)) + x % SUB; };  // in [i0, i1): < nt
+      auto start_of = [&](int i) { return 16 * (i0 + i < u.st ? i0 + i : u.wt0 + i0 + i - u.st); };
+      const int n_pages = (int)kv.n_pages;
+      auto look = [&](int x, int& page, int& slot) {
+        page = -2;  // no such tile
+        slot = 0;
+        const int i = tile_of(x);
+        if (i < nt) {
+          const int t = start_of(i), e = t / kv.page_size;
+          slot = t - e * kv.page_size;
+          page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
+          if (page == -2) page = -1;
+        }
+      };
+      int pages, pages1, slots, slots1;
+      look(lane, pages, slots);
+      look(32 + lane, pages1, slots1);
+
       // ---- Q fragments (B operand) in the order of the reduction axis that the K fragments have
       const bool head_ok = gq < G;
       const __nv_bfloat16* qrow =
@@ -265,28 +295,6 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       // of a visible token so far, so that weight * scale is at most 1
       int e_acc = -1000;
 
-      // ---- this warp's tiles, SUB at a time: i0 + SUB (warp + 4 it) + u of
-      // iteration it; lane k keeps the pages of its tiles 32 j + k (in that
-      // order), the next 32 looked up while these are used
-      const int nt = i1 - i0;
-      const int n_it = max(0, ((nt + SUB - 1) / SUB - warp + kWarps - 1) / kWarps);
-      auto tile_of = [&](int x) { return SUB * (warp + kWarps * (x / SUB)) + x % SUB; };  // in [i0, i1): < nt
-      auto start_of = [&](int i) { return 16 * (i0 + i < u.st ? i0 + i : u.wt0 + i0 + i - u.st); };
-      const int n_pages = (int)kv.n_pages;
-      auto look = [&](int x, int& page, int& slot) {
-        page = -2;  // no such tile
-        slot = 0;
-        const int i = tile_of(x);
-        if (i < nt) {
-          const int t = start_of(i), e = t / kv.page_size;
-          slot = t - e * kv.page_size;
-          page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
-          if (page == -2) page = -1;
-        }
-      };
-      int pages, pages1, slots, slots1;
-      look(lane, pages, slots);
-      look(32 + lane, pages1, slots1);
       auto page_of = [&](int x, int j) { return __shfl_sync(0xffffffffu, (x >> 5) == j ? pages : pages1, x & 31); };
       auto issue = [&](int it, int j) {  // every lane; a few of them copy
         const uint32_t s = (gi + (uint32_t)it) % R::kStages;
@@ -648,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       off = 0;
       if (++g == Hkv) {
         g = 0;
-        if (++b < B) u = unit_of(a, b, nullptr);
+        if (++b < B) u = unit_of(a, paged_tokens(kv, b, nullptr));
       }
     } else {
       off += take;
