@@ -67,7 +67,10 @@ namespace sa {
 namespace {
 
 constexpr int kC0 = 2;              // cost of starting a pair, in blocks
-constexpr int kMinShare = 4 + kC0;  // least work of a CTA
+// Least work of a CTA: small calls are a chain of latencies and so spread widely
+// (16 rows over 2k tokens, 4 KV heads, in a graph: 20.6 us; shares of 4 and 6:
+// 21.4 and 25.7).
+constexpr int kMinShare = kC0 + 1;
 constexpr int kInfo = 16;
 constexpr int BLK = 64;             // tokens of a block
 constexpr int NR = 4;               // tiles of codes in flight (K, V alternating)
@@ -230,9 +233,11 @@ struct Cursor {
   }
 };
 
-// Work of the sequences b (one per thread of a converged warp), one KV head.
-SA_DEV unsigned long long seq_work(const ChunkArgs& a, int b) {
-  int N = 0, m = 0, r0;
+// Work of the sequences b (one per thread of a converged warp), one KV head;
+// their tokens and new rows.
+SA_DEV unsigned long long seq_work(const ChunkArgs& a, int b, int& N, int& m) {
+  int r0;
+  N = m = 0;
   if (b < a.p.kv.B) {
     m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, a.p.status);
     N = paged_tokens(a.p.kv, b, a.p.status);
@@ -278,27 +283,84 @@ SA_DEV unsigned long long scan64(unsigned long long v, unsigned long long* scrat
   return base + x - v;
 }
 
-// This CTA's share of the work (every thread calls it; scratch: 30 words).
-SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratch) {
-  const int T = blockDim.x, tid = threadIdx.x, B = a.p.kv.B;
-  const unsigned long long H = a.p.kv.Hkv;
-  unsigned long long total = 0, w = 0, w1 = 0, t, ex = 0;
-  for (int base = 0; base < B; base += T) {
-    w1 = seq_work(a, base + tid);
-    w = w1 * H;
-    ex = scan64(w, scratch, t) + total;
-    total += t;
+// The pair of sequence (N, m) that holds unit `off` of one head's work (a warp).
+SA_DEV void find_pair(const ChunkArgs& a, int N, int m, unsigned long long off, Plan* plan) {
+  const int lane = threadIdx.x & 31, pairs = (m + 2 * a.R - 1) / (2 * a.R);
+  unsigned long long before = 0;
+  for (int j0 = 0; j0 < pairs; j0 += 32) {
+    const int j = j0 + lane;
+    const unsigned long long cst = j < pairs ? pair_geom(a, N, m, j).nb + kC0 : 0;
+    unsigned long long x = cst;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    x += before;
+    if (cst && x - cst <= off && off < x) {
+      plan->j = j;
+      plan->off = (int)(off - (x - cst));
+    }
+    before = __shfl_sync(0xffffffffu, x, 31);
   }
+}
+
+// This CTA's run of a list of `total` work.
+SA_DEV void share(unsigned long long total, Plan* plan) {
   // as many CTAs as have kMinShare each; the first `more` of them take one unit more than `each`
   const unsigned n = total >= (unsigned long long)gridDim.x * kMinShare ? gridDim.x : max(1u, (unsigned)total / kMinShare);
   const unsigned c = blockIdx.x;
   const unsigned long long each = total >> 32 ? total / n : (unsigned)total / n;
   const unsigned more = (unsigned)(total - each * n);
+  plan->each = each;
+  plan->more = more;
+  plan->w0 = c < n ? each * c + min(c, more) : 0;
+  plan->w1 = c < n ? plan->w0 + each + (c < more ? 1u : 0u) : 0;
+}
+
+// This CTA's share of the work (every thread calls it; scratch: 30 words; the
+// caller synchronises before the plan is read).
+SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratch) {
+  const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, B = a.p.kv.B;
+  const unsigned long long H = a.p.kv.Hkv;
+  if (B <= 32) {  // one warp, without block barriers (a third of the 5000 cycles)
+    if (tid >= 32) return;
+    int N = 0, m = 0;
+    const unsigned long long per = seq_work(a, lane, N, m), w = per * H;
+    unsigned long long x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    Plan p;
+    share(__shfl_sync(0xffffffffu, x, 31), &p);
+    p.b = B;
+    p.g = p.j = p.off = 0;
+    const unsigned here = __ballot_sync(0xffffffffu, w && x - w <= p.w0 && p.w0 < x);
+    if (p.w1 != p.w0 && here) {
+      p.b = __ffs(here) - 1;
+      const unsigned long long in = p.w0 - __shfl_sync(0xffffffffu, x - w, p.b), one = __shfl_sync(0xffffffffu, per, p.b);
+      p.g = (in >> 32) || (one >> 32) ? (int)(in / one) : (int)((unsigned)in / (unsigned)one);
+      if (lane == 0) *plan = p;
+      __syncwarp();
+      find_pair(a, __shfl_sync(0xffffffffu, N, p.b), __shfl_sync(0xffffffffu, m, p.b), in - (unsigned long long)p.g * one,
+                plan);
+    } else if (lane == 0) {
+      *plan = p;
+    }
+    return;
+  }
+  unsigned long long total = 0, w = 0, w1 = 0, t, ex = 0;
+  int N, m;
+  for (int base = 0; base < B; base += T) {
+    w1 = seq_work(a, base + tid, N, m);
+    w = w1 * H;
+    ex = scan64(w, scratch, t) + total;
+    total += t;
+  }
   if (tid == 0) {
-    plan->each = each;
-    plan->more = more;
-    plan->w0 = c < n ? each * c + min(c, more) : 0;
-    plan->w1 = c < n ? plan->w0 + each + (c < more ? 1u : 0u) : 0;
+    share(total, plan);
     plan->b = B;
     plan->g = plan->j = plan->off = 0;
   }
@@ -308,7 +370,7 @@ SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratc
   unsigned long long run = 0;
   for (int base = 0; base < B; base += T) {
     if (B > T) {
-      w1 = seq_work(a, base + tid);
+      w1 = seq_work(a, base + tid, N, m);
       w = w1 * H;
       ex = scan64(w, scratch, t) + run;
       run += t;
@@ -323,30 +385,12 @@ SA_DEV void make_plan(const ChunkArgs& a, Plan* plan, unsigned long long* scratc
   if (tid < 32) {
     const unsigned long long in = scratch[28], per = scratch[29];
     const int b = plan->b, g = (in >> 32) || (per >> 32) ? (int)(in / per) : (int)((unsigned)in / (unsigned)per);
-    const unsigned long long off = in - (unsigned long long)g * per;
     int r0;
-    const int m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, nullptr), N = paged_tokens(a.p.kv, b, nullptr);
-    const int pairs = (m + 2 * a.R - 1) / (2 * a.R);
-    unsigned long long before = 0;
-    for (int j0 = 0; j0 < pairs; j0 += 32) {
-      const int j = j0 + tid;
-      const unsigned long long cst = j < pairs ? pair_geom(a, N, m, j).nb + kC0 : 0;
-      unsigned long long x = cst;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (tid >= o) x += y;
-      }
-      x += before;
-      if (cst && x - cst <= off && off < x) {
-        plan->g = g;
-        plan->j = j;
-        plan->off = (int)(off - (x - cst));
-      }
-      before = __shfl_sync(0xffffffffu, x, 31);
-    }
+    m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, nullptr);
+    N = paged_tokens(a.p.kv, b, nullptr);
+    if (tid == 0) plan->g = g;
+    find_pair(a, N, m, in - (unsigned long long)g * per, plan);
   }
-  __syncthreads();
 }
 
 // 4 codes -> two bf16 pairs: a code's 7 low bits are the exponent and mantissa
@@ -784,10 +828,12 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
           unpack_f2(rq[1], s2, s3);
           sum = (s0 + s1) + (s2 + s3);
         };
-        scores();
-        weights();
+        if (used) {
+          scores();
+          weights();
+        }
         // (a sum that is NaN because scores are does not ask for it, nor do lanes without a vector)
-        if (pair_any(id, vok && (sum > 0x1p20f || mref == ninf))) {
+        if (!used || pair_any(id, vok && (sum > 0x1p20f || mref == ninf))) {
           // S is still in place: the scores need not be kept for this
           scores();
           // rare: the row's maximum over both halves, and what follows from it
@@ -827,7 +873,7 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
           weights();
         }
         lh += sum;
-        // P lies over S: the other half's scores have been read (pair_any)
+        // P lies over S: the other half's scores have been read (pair_any, pair_sync)
         tc::st_32x32b_x16(tb + 16 * half, p1);
         if constexpr (TERMS == 3) {
 #pragma unroll
