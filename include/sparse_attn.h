@@ -421,9 +421,10 @@ sa_status sparse_attn_decode_static(const sa_kv_desc* kv, const void* q, int32_t
  * range outside [0, n_rows] counts as having no tokens or no rows; rows
  * before the sequence's first token (m_b > N_b) are not stored and see
  * nothing (an empty slot of a decode batch, N_b = 0, is no error: its row of
- * sparse_attn_paged_decode sees nothing); a token whose page is outside [0, n_pages) is not stored, not read
- * and not attended.  Pages that no token of the call needs are not looked at
- * (entries of pages that a window has passed may hold anything). */
+ * sparse_attn_paged_decode sees nothing); a token whose page is outside
+ * [0, n_pages) is not stored, not read and not attended.  Pages that no token
+ * of the call needs are not looked at (entries of pages that a window has
+ * passed may hold anything). */
 typedef enum {
   SA_KV_BF16 = 0,
   SA_KV_E4M3 = 1
