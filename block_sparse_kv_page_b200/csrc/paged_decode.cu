@@ -4,6 +4,9 @@
 // head g: out = sum exp(z_t - lse) v_t over the visible tokens, z_t = scale
 // q . k_t, in one pass with a running maximum and sum.  Every visible token's K
 // and V are read once for the G <= 8 heads that share them; that read bounds it.
+// Measured: 32 sequences of up to 32k tokens, 8 KV heads, e4m3: 224 us, 5.1
+// TB/s; one of 29.5k tokens, 4 KV heads, bf16: 21 us, where the read itself
+// takes 9.4 and the rest is latency (lengths, table, first tiles, merge).
 //
 // Units are (sequence, KV head) pairs, cut into tiles of 16 tokens (those of
 // the first tokens and of the window; a page is whole tiles).  The work is the
