@@ -921,6 +921,9 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
         }
         pair_sync(id);
         if (half == 0) lh = *xr;
+        // (the maximum passes over NaN scores: where there was nothing else, the
+        // merges would take the part for one that saw no token)
+        if (lh != lh) mref = fmaxf(mref, 0.f);
       }
       if (used) {
         wait(o_done + 2 * t + ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u);
@@ -950,7 +953,7 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
       } else if (!whole) {
         part = a.parts + (((size_t)blockIdx.x * 2 + (sg.i0 == 0 ? 1 : 0)) * 2 + t) * kChunkPart;
       }
-      const float inv = part ? 1.f : (lh > 0.f ? 1.f / lh : 0.f);
+      const float inv = part ? 1.f : (lh != 0.f ? 1.f / lh : 0.f);
       const size_t orow = vok ? (size_t)(sg.row0 + row) * a.p.Hq + (size_t)sg.g * G + hh : 0;
       const bool mine = vok && !dead && !(sg.single && t == 1 && sg.nb == 0);  // (then slot 0 writes the zeros)
       f0 *= inv;
@@ -1063,7 +1066,7 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
       }
       if (mine && half == 0) {
         if (part) *reinterpret_cast<float2*>(part + kChunkMl + 2 * r) = make_float2(mref, lh);
-        else if (a.p.lse) a.p.lse[orow] = lh > 0.f ? mref * kLn2 + logf(lh) : ninf;
+        else if (a.p.lse) a.p.lse[orow] = lh != 0.f ? mref * kLn2 + logf(lh) : ninf;
         if (sg.i0 == 0 && qpos < 0) flag_status(status, SA_ERR_DEVICE_CHECK);
       }
       if (merge) {
@@ -1146,7 +1149,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
       M = nm;
     }
     if (!ok) continue;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L != 0.f ? 1.f / L : 0.f;
 #pragma unroll
     for (int x = 0; x < 2; ++x) o[x] = make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
     const size_t orow = (size_t)(rec.row0 + row) * a.p.Hq + (size_t)rec.g * G + (r - rr * G);
@@ -1158,7 +1161,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
       *reinterpret_cast<uint4*>(a.p.out_bf16 + orow * kHeadDim + 4 * d4) =
           make_uint4(pack_bf16(o[0].x, o[0].y), pack_bf16(o[0].z, o[0].w), pack_bf16(o[1].x, o[1].y), pack_bf16(o[1].z, o[1].w));
     }
-    if (a.p.lse && d4 == 0) a.p.lse[orow] = L > 0.f ? M * kLn2 + logf(L) : ninf;
+    if (a.p.lse && d4 == 0) a.p.lse[orow] = L != 0.f ? M * kLn2 + logf(L) : ninf;
   }
 }
 

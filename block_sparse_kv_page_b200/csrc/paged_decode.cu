@@ -590,6 +590,10 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
         l0 += __shfl_xor_sync(0xffffffffu, l0, o);
         l1 += __shfl_xor_sync(0xffffffffu, l1, o);
       }
+      // (the maximum passes over NaN scores: where there was nothing else, the
+      // merges would take the part for one that saw no token)
+      if (l0 != l0) m0 = fmaxf(m0, 0.f);
+      if (l1 != l1) m1 = fmaxf(m1, 0.f);
       __syncthreads();  // the rings are no longer read
       float* w_acc = reinterpret_cast<float*>(base);               // [warp][8][128]
       float* w_ml = w_acc + kWarps * kMaxGroup * kHeadDim;         // [warp][8][2]
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           *reinterpret_cast<float4*>(dst + d0 + 4) = make_float4(A[4], A[5], A[6], A[7]);
           if (d0 == 0) *reinterpret_cast<float2*>(dst + kHeadDim) = make_float2(M, L);
         } else {
-          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const float inv = L != 0.f ? 1.f / L : 0.f;
           if (a.p.out) {
             float* o = a.p.out + row * kHeadDim + d0;
             *reinterpret_cast<float4*>(o) = make_float4(A[0] * inv, A[1] * inv, A[2] * inv, A[3] * inv);
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
                 make_uint4(pack_bf16(A[0] * inv, A[1] * inv), pack_bf16(A[2] * inv, A[3] * inv),
                            pack_bf16(A[4] * inv, A[5] * inv), pack_bf16(A[6] * inv, A[7] * inv));
           }
-          if (a.p.lse && d0 == 0) a.p.lse[row] = L > 0.f ? M * kLn2 + logf(L) : ninf;
+          if (a.p.lse && d0 == 0) a.p.lse[row] = L != 0.f ? M * kLn2 + logf(L) : ninf;
         }
       }
       if (tid == 0 && i0 == 0) {  // whether, and up to which CTA, the unit goes on
@@ -737,14 +741,14 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const __grid_consta
       o.w += v.w * e;
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   const size_t row = (size_t)rec.z * a.p.Hq + (size_t)rec.w * G + h;
   if (a.p.out)
     *reinterpret_cast<float4*>(a.p.out + row * kHeadDim + 4 * lane) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   else
     *reinterpret_cast<uint2*>(a.p.out_bf16 + row * kHeadDim + 4 * lane) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (a.p.lse && lane == 0) a.p.lse[row] = L > 0.f ? M * kLn2 + logf(L) : ninf;
+  if (a.p.lse && lane == 0) a.p.lse[row] = L != 0.f ? M * kLn2 + logf(L) : ninf;
 }
 
 template <bool E4M3, int TERMS>

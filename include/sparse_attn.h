@@ -437,7 +437,7 @@ typedef struct {
   int32_t page_size;          /* tokens of a page: multiple of 16 in [16, 256] */
   int64_t n_pages;            /* pages of the pool, 1 .. 2^31 - 1 */
   int32_t dtype;              /* sa_kv_dtype of k and v */
-  int32_t max_pages;          /* page table entries of a sequence; max_pages * page_size < 2^31 */
+  int32_t max_pages;          /* page table entries of a sequence; max_pages * page_size <= 2^31 - 256 */
   void* k;                    /* value d of (page, head, slot) at k + page * page_stride + head * */
   void* v;                    /*   head_stride + slot * token_stride + d; 16-byte aligned */
   int64_t page_stride;        /* elements, positive multiples of 16 bytes; so head-major and */
@@ -485,7 +485,9 @@ sa_status sparse_attn_cache_read(const sa_paged_desc* kv, int32_t first_token, v
  * bf16 (16-byte aligned); lse (nullable) fp32 [n_rows][n_q_heads], the natural
  * logarithm of the sum of exp(z).  A row that sees nothing gets out = 0 and
  * lse = -inf.  What is held past N_b, or where no row of the sequence looks,
- * may be anything, NaN included.  Any m_b from 0 on; lengths are read on the
+ * may be anything, NaN included; a NaN in q, or in a bf16 key that a row sees,
+ * makes that row NaN (a NaN code of an e4m3 row that is seen, and infinities,
+ * give undefined results).  Any m_b from 0 on; lengths are read on the
  * device only, so a captured call replays with other lengths.  Two launches. */
 sa_status sparse_attn_chunk(const sa_paged_desc* kv, const void* q, int64_t q_row_stride,
                             int32_t n_q_heads, const int32_t* row_off, int32_t n_rows,

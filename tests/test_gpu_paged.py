@@ -465,6 +465,41 @@ def test_row_scales_far_apart(cuda_dev, sa, out, decode):
     c.check(c.run(50, 3, decode=decode), 50, 3)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("longest", [40, 9000])
+def test_nan_queries_give_nan_and_leave_others_alone(cuda_dev, sa, cache, decode, longest):
+    """A NaN in q makes its own row and head NaN, output and lse, whether the
+    row lies in one part or in many; every other row is as it was."""
+    lens = [longest, 33, longest // 2]
+    rows = [1] * 3 if decode else [20, 3, 7]
+    c = Case(sa, cuda_dev, lens=lens, rows=rows, hq=8, hkv=2, page=16, cache=cache, seed=93)
+    c.dq[1, 3, 5] = float("nan")
+    c.dq[2, 7] = float("nan")
+    out, lse = c.run(decode=decode)
+    for r, h in ((1, 3), (2, 7)):
+        assert torch.isnan(out[r, h]).all() and torch.isnan(lse[r, h])
+    c.dq.copy_(c.q)
+    want = c.run(decode=decode)
+    for r, h in ((1, 3), (2, 7)):
+        out[r, h], lse[r, h] = want[0][r, h], want[1][r, h]
+    c.check(want)
+    c.check((out, lse))
+
+
+def test_nan_in_a_row_of_the_cache_reaches_the_rows_that_see_it(cuda_dev, sa):
+    """bf16 cache: a NaN key makes the heads that share it NaN in the decode of
+    its sequence, and leaves the other sequences and heads alone."""
+    c = Case(sa, cuda_dev, lens=[5000, 70], rows=[1, 1], hq=8, hkv=2, page=16, cache="bf16", seed=94)
+    want = c.run(decode=True)
+    page, slot = int(c.table[0, 1234 // 16]), 1234 % 16
+    c.dk[page, 1, slot, 9] = float("nan")
+    out, lse = c.run(decode=True)
+    assert torch.isnan(out[0, 4:]).all() and torch.isnan(lse[0, 4:]).all()
+    assert torch.equal(out[0, :4], want[0][0, :4]) and torch.equal(out[1], want[0][1])
+    assert torch.equal(lse[0, :4], want[1][0, :4]) and torch.equal(lse[1], want[1][1])
+
+
 def test_offsets_past_32_bits(cuda_dev, sa):
     """Pages 1.5 GiB apart: element and byte offsets pass 2^32."""
     far, n_pages = 3 << 29, 6
