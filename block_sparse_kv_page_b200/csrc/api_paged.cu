@@ -75,7 +75,8 @@ sa_status check_paged(const sa_paged_desc* kv) {
   if (kv->dtype != SA_KV_BF16 && kv->dtype != SA_KV_E4M3) return SA_ERR_INVALID;
   if (kv->head_dim != kHeadDim) return SA_ERR_UNSUPPORTED;
   if (kv->page_size % 16 != 0 || kv->page_size < 16 || kv->page_size > 256) return SA_ERR_UNSUPPORTED;
-  if (kv->n_pages > 0x7fffffffLL || (long long)kv->max_pages * kv->page_size > 0x7fffffffLL)
+  // (blocks of up to 64 tokens are counted, and ended, in 32 bits)
+  if (kv->n_pages > 0x7fffffffLL || (long long)kv->max_pages * kv->page_size > 0x7fffff00LL)
     return SA_ERR_UNSUPPORTED;
   if (!kv->k || !kv->v || !aligned(kv->k, 16) || !aligned(kv->v, 16)) return SA_ERR_INVALID;
   const int64_t step = kv->dtype == SA_KV_E4M3 ? 16 : 8;  // elements of 16 bytes

@@ -203,3 +203,13 @@ def test_workspace_size_through_the_binding():
     n = sa.sparse_attn_paged_workspace_size(c, 8)
     assert n > 256 and n % 256 == 0
     assert sa.sparse_attn_paged_workspace_size(c, 7) == 0
+
+
+def test_longest_sequence(abi, lib):
+    """Lengths are held, and blocks of 64 tokens ended, in 32 bits."""
+    for pages, page in (((1 << 27) - 1, 16), ((1 << 23) - 1, 256), ((1 << 25) - 1, 64)):
+        ok = pages * page <= 2 ** 31 - 256
+        kv = _desc(abi, max_pages=pages, page_size=page)
+        assert (lib.sparse_attn_paged_workspace_size(C.byref(kv), 32) > 0) == ok
+        if not ok:
+            assert set(_calls(lib, abi, kv).values()) == {abi.SA_ERR_UNSUPPORTED}
