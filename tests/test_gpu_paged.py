@@ -614,6 +614,26 @@ def test_many_sequences(cuda_dev, sa):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 127, 128, 129, 640, 641, 897])
+def test_sequence_counts_around_a_warp_and_a_block(cuda_dev, sa, B):
+    """Where the plan of the work changes hands: a warp, a block, several rounds."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    lens[B // 2], lens[B - 1] = 900, 33
+    c = Case(sa, cuda_dev, lens=lens, rows=[1] * B, hq=2, hkv=1, page=16, cache="bf16", seed=B)
+    c.check(c.run(decode=True))
+    rows = [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 5, B))]
+    for cache in ("bf16", "e4m3") if B < 600 or B == 897 else ("bf16",):
+        c = Case(sa, cuda_dev, lens=lens, rows=rows, hq=2, hkv=1, page=16, cache=cache, seed=B)
+        c.check(c.run())
+
+
+def test_long_chunks_of_many_tiles(cuda_dev, sa):
+    """More pairs of tiles than a warp has lanes, in the first and the last sequence."""
+    c = Case(sa, cuda_dev, lens=[1150, 40, 1300], rows=[1150, 0, 1090], hq=8, hkv=1, page=32, out="bf16", seed=181)
+    c.check(c.run(100, 3), 100, 3)
+
+
 # ---------------------------------------------------------------- as a run
 @pytest.mark.parametrize("window,sinks", [(0, 0), (96, 4)])
 def test_prompt_then_tokens_as_they_are_served(cuda_dev, sa, window, sinks):
