@@ -409,11 +409,12 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
               mma_bf16(k & 1 ? s2 : s, a0, a1, a2, a3, bq[2 * k], bq[2 * k + 1]);
             }
           }
-          // tokens gq / gq + 8, heads 2 c / 2 c + 1
-          z[y][0] = v0[y] ? (s[0] + s2[0]) * ka * zs0 : ninf;
-          z[y][1] = v0[y] ? (s[1] + s2[1]) * ka * zs1 : ninf;
-          z[y][2] = v1[y] ? (s[2] + s2[2]) * kb * zs0 : ninf;
-          z[y][3] = v1[y] ? (s[3] + s2[3]) * kb * zs1 : ninf;
+          // tokens gq / gq + 8, heads 2 c / 2 c + 1; q's scale first: sums of scaled
+          // values times a huge key scale would overflow where the score does not
+          z[y][0] = v0[y] ? (s[0] + s2[0]) * zs0 * ka : ninf;
+          z[y][1] = v0[y] ? (s[1] + s2[1]) * zs1 * ka : ninf;
+          z[y][2] = v1[y] ? (s[2] + s2[2]) * zs0 * kb : ninf;
+          z[y][3] = v1[y] ? (s[3] + s2[3]) * zs1 * kb : ninf;
           mx0 = fmaxf(mx0, fmaxf(z[y][0], z[y][2]));
           mx1 = fmaxf(mx1, fmaxf(z[y][1], z[y][3]));
         }

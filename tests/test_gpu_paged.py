@@ -500,6 +500,20 @@ def test_nan_in_a_row_of_the_cache_reaches_the_rows_that_see_it(cuda_dev, sa):
     assert torch.equal(lse[0, :4], want[1][0, :4]) and torch.equal(lse[1], want[1][1])
 
 
+@pytest.mark.parametrize("power", [-112, -90, 90, 110])
+@pytest.mark.parametrize("decode", [False, True])
+def test_key_scales_near_the_ends_of_the_range(cuda_dev, sa, decode, power):
+    """Ordinary scores from tiny queries and huge keys, and the other way round."""
+    c = Case(sa, cuda_dev, lens=[700, 40], rows=[1, 1] if decode else [9, 2], hq=8, hkv=2, page=16, cache="e4m3",
+             seed=97)
+    # queries times 2^power (exact in bf16: normal powers), keys times 2^-power
+    c.q = (c.q.float() * 2.0 ** power).to(torch.bfloat16)
+    c.dq.copy_(c.q)
+    c.ks = (c.ks.int() - power).to(torch.uint8)
+    c.dks.copy_(c.ks)
+    c.check(c.run(decode=decode))
+
+
 def test_offsets_past_32_bits(cuda_dev, sa):
     """Pages 1.5 GiB apart: element and byte offsets pass 2^32."""
     far, n_pages = 3 << 29, 6
