@@ -136,7 +136,7 @@ sa_status check_heads(const sa_paged_desc* kv, int n_q_heads, int* G) {
 
 // Tensor maps of the pool, [n_pages][Hkv][page_size][128], boxes of `rows` rows
 // of 128 bytes (64 bf16 or 128 codes).
-bool cache_maps(const PagedView& kv, CUtensorMap* k, CUtensorMap* v, int rows, bool swizzle) {
+bool cache_maps(const PagedView& kv, CUtensorMap* k, CUtensorMap* v, int rows) {
   const unsigned long long d[4] = {kHeadDim, (unsigned long long)kv.page_size, (unsigned long long)kv.Hkv,
                                    (unsigned long long)kv.n_pages};
   const unsigned long long s[3] = {(unsigned long long)kv.token_stride, (unsigned long long)kv.head_stride,
@@ -145,8 +145,8 @@ bool cache_maps(const PagedView& kv, CUtensorMap* k, CUtensorMap* v, int rows, b
   const CUtensorMapDataType dt = kv.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   // (rows of 128 codes, token by token: with 256-byte fetches L2 brought the
   // neighbouring head's row along, 1.5 times the bytes)
-  return encode_tmap_nd(k, kv.k, dt, 4, d, s, b, swizzle, !kv.e4m3) &&
-         encode_tmap_nd(v, kv.v, dt, 4, d, s, b, swizzle, !kv.e4m3);
+  return encode_tmap_nd(k, kv.k, dt, 4, d, s, b, true, !kv.e4m3) &&
+         encode_tmap_nd(v, kv.v, dt, 4, d, s, b, true, !kv.e4m3);
 }
 
 sa_status decode(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
@@ -154,7 +154,7 @@ sa_status decode(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   const PagedView& kv = p.kv;
   a.p = p;
   a.scale_log2 = p.scale * kLog2e;
-  if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, 16, true)) return SA_ERR_CUDA;
+  if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, 16)) return SA_ERR_CUDA;
   const int grid = paged_decode_grid(device_sm_count());
   const long long units = (long long)kv.B * kv.Hkv;
   a.by_unit = units <= grid ? 1 : 0;
@@ -178,7 +178,7 @@ sa_status chunk(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   const unsigned qb[3] = {64, (unsigned)p.G, (unsigned)a.R};
   if (!encode_tmap_nd(&a.tmap_q, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, qd, qs, qb, true, true)) return SA_ERR_CUDA;
   // bf16: halves of 64 dims, swizzled for the MMA; e4m3: whole rows of codes
-  if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, a.hb, !kv.e4m3)) return SA_ERR_CUDA;
+  if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, a.hb)) return SA_ERR_CUDA;
   const PagedScratch sc = paged_scratch();
   a.parts = (float*)(ws + sc.parts);
   a.xbuf = (float*)(ws + sc.xbuf);

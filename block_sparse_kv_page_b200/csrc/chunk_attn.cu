@@ -679,11 +679,15 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
       mbar_wait(drain, 0, nullptr);
     }
   } else if (warp >= 20) {
-    // ---- e4m3 -> bf16: 8 threads per row, 16 rows at a time
+    // ---- e4m3 -> bf16: 8 threads per row, 16 rows at a time.  Eight lanes in a
+    // row take half of rows r and r ^ 5: under both swizzles their 16-byte pieces
+    // then fall into different banks, of the codes (rows that differ in bit 2)
+    // and of the bf16 tile, where a lane has two (rows that differ in bit 0).
     if constexpr (E4M3) {
       reg_dealloc<Regs<E4M3>::kConvert>();
       const int w = (warp - 20) >> 2;  // K or V
-      const int x = (tid - 640) & 127, c = x & 7, r16 = x >> 3;
+      const int c = (lane & 3) | ((lane >> 1) & 4), j = 2 * (warp & 3) + (lane >> 4);
+      const int r16 = ((j & 3) | ((j & 4) << 1)) ^ (lane & 4 ? 5 : 0);
       int n = 0;
       bool ok = true;
       while (ok && cur.next(a, sg)) {
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
             uint32_t sc[BLK / 16];
 #pragma unroll
             for (int s = 0; s < BLK / 16; ++s) {
-              code[s] = lds128(raw + rs * Sh::kRaw + (16 * s + r16) * 128 + 16 * c);
+              code[s] = lds128(raw + rs * Sh::kRaw + swz128(16 * s + r16, c));
               sc[s] = raw_scale[rs * BLK + 16 * s + r16];
             }
             if (edge) {
