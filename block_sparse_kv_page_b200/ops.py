@@ -438,22 +438,22 @@ def _paged_call(kv: PagedCache, fn, where: str, *args) -> None:
 def _rows(t: torch.Tensor, name: str, heads: int | None = None) -> int:
     """The row stride (elements) of a packed bf16 [rows, heads, 128] array
     whose heads lie one after another, so parts of a projection's rows fit."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be a bf16 [rows, heads, 128] tensor of the call's heads")
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != 128 and t.shape[1] > 1):
+    if s2 != 1 or (s1 != 128 and shape[1] > 1):
         raise ValueError(f"{name} must have its heads one after another in a row")
-    return s0 if t.shape[0] > 1 else t.shape[1] * 128
+    return s0 if shape[0] > 1 else shape[1] * 128
 
 
 def _row_off(row_off: torch.Tensor, kv: PagedCache) -> None:
-    if row_off.dtype != torch.int32 or row_off.dim() != 1 or row_off.shape[0] != kv.batch + 1 \
-            or not row_off.is_contiguous():
+    if row_off.dtype is not torch.int32 or row_off.shape != (kv.batch + 1,) or not row_off.is_contiguous():
         raise ValueError("row_off must be contiguous int32 [B + 1]")
 
 
 def _ws(ws: torch.Tensor | None) -> tuple[int | None, int]:
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
 def sparse_attn_paged_workspace_size(kv: PagedCache, n_q_heads: int) -> int:
@@ -483,14 +483,15 @@ def sparse_attn_cache_write(kv: PagedCache, k_new: torch.Tensor, v_new: torch.Te
     quantised if it holds e4m3.  ws: takes the status word; may be None."""
     Hkv = kv.n_kv_heads
     stride = _rows(k_new, "k_new", Hkv)
-    if v_new.shape[0] != k_new.shape[0] or _rows(v_new, "v_new", Hkv) != stride:
+    rows = k_new.shape[0]
+    if v_new.shape[0] != rows or _rows(v_new, "v_new", Hkv) != stride:
         raise ValueError("k_new and v_new must have the same rows and strides")
     _row_off(row_off, kv)
     s = _on(kv, stream, k_new, v_new, row_off, ws)
-    if k_new.shape[0] == 0:
+    if rows == 0:
         return
     _paged_call(kv, lib.sparse_attn_cache_write, "sparse_attn_cache_write", kv.ref, k_new.data_ptr(),
-                v_new.data_ptr(), stride, row_off.data_ptr(), k_new.shape[0], *_ws(ws), s)
+                v_new.data_ptr(), stride, row_off.data_ptr(), rows, *_ws(ws), s)
 
 
 def sparse_attn_cache_read(kv: PagedCache, first_token: int, k_out: torch.Tensor, v_out: torch.Tensor,
@@ -507,12 +508,13 @@ def sparse_attn_cache_read(kv: PagedCache, first_token: int, k_out: torch.Tensor
                 k_out.data_ptr(), v_out.data_ptr(), k_out.shape[2], *_ws(ws), s)
 
 
-def _attn_out(q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None) -> int:
-    if out.shape != q.shape or not out.is_contiguous() or out.dtype not in (torch.float32, torch.bfloat16):
+def _attn_out(rows: int, heads: int, out: torch.Tensor, lse: torch.Tensor | None) -> int:
+    dtype = out.dtype
+    if out.shape != (rows, heads, 128) or not out.is_contiguous() or dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("out must be contiguous fp32 or bf16 [rows, Hq, 128]")
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != q.shape[:2]):
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.shape != (rows, heads)):
         raise ValueError("lse must be contiguous fp32 [rows, Hq]")
-    return _abi.SA_OUT_BF16 if out.dtype == torch.bfloat16 else _abi.SA_OUT_F32
+    return _abi.SA_OUT_BF16 if dtype is torch.bfloat16 else _abi.SA_OUT_F32
 
 
 def sparse_attn_chunk(kv: PagedCache, q: torch.Tensor, row_off: torch.Tensor, scale: float, window: int, sinks: int,
@@ -522,13 +524,14 @@ def sparse_attn_chunk(kv: PagedCache, q: torch.Tensor, row_off: torch.Tensor, sc
     keys and values the cache already holds) over the cache.  window > 0: a row
     sees its last `window` tokens, itself included, and the first `sinks`."""
     stride = _rows(q, "q")
-    out_dtype = _attn_out(q, out, lse)
+    rows, heads, _ = q.shape
+    out_dtype = _attn_out(rows, heads, out, lse)
     _row_off(row_off, kv)
     s = _on(kv, stream, q, row_off, out, lse, ws)
-    if q.shape[0] == 0:
+    if rows == 0:
         return
-    _paged_call(kv, lib.sparse_attn_chunk, "sparse_attn_chunk", kv.ref, q.data_ptr(), stride, q.shape[1],
-                row_off.data_ptr(), q.shape[0], int(window), int(sinks), float(scale), out.data_ptr(), out_dtype,
+    _paged_call(kv, lib.sparse_attn_chunk, "sparse_attn_chunk", kv.ref, q.data_ptr(), stride, heads,
+                row_off.data_ptr(), rows, int(window), int(sinks), float(scale), out.data_ptr(), out_dtype,
                 _ptr(lse), *_ws(ws), s)
 
 
@@ -537,9 +540,10 @@ def sparse_attn_paged_decode(kv: PagedCache, q: torch.Tensor, scale: float, wind
     """One row per sequence: q bf16 [B, Hq, 128], row b the newest token of
     sequence b; otherwise as sparse_attn_chunk."""
     stride = _rows(q, "q")
-    if q.shape[0] != kv.batch:
+    rows, heads, _ = q.shape
+    if rows != kv.batch:
         raise ValueError("q must have one row per sequence")
-    out_dtype = _attn_out(q, out, lse)
+    out_dtype = _attn_out(rows, heads, out, lse)
     s = _on(kv, stream, q, out, lse, ws)
     _paged_call(kv, lib.sparse_attn_paged_decode, "sparse_attn_paged_decode", kv.ref, q.data_ptr(), stride,
-                q.shape[1], int(window), int(sinks), float(scale), out.data_ptr(), out_dtype, _ptr(lse), *_ws(ws), s)
+                heads, int(window), int(sinks), float(scale), out.data_ptr(), out_dtype, _ptr(lse), *_ws(ws), s)
