@@ -29,9 +29,10 @@
 // pieces of a row: 32 dims of two tokens for K, 16 dims of four tokens for V,
 // free of bank conflicts under the swizzle.  Codes become f16, one conversion per
 // pair: q is scaled per head to fit, and weights times V's scales are taken
-// relative to the largest scale seen, which is followed like the maximum; rows
-// whose scale lies far below it take the same products in bf16 (whose
-// conversion, by shifts and masks, costs three times as much).  The rows' scales (powers of two)
+// relative to the largest scale seen, which is followed like the maximum; tiles
+// with a weight below what f16 holds take the same products in bf16 (whose
+// conversion, by shifts and masks, costs three times as much: 16 sequences of
+// 32k tokens 183 us, 220 where every tile takes it).  The rows' scales (powers of two)
 // multiply the scores and the weights, 4 values a lane instead of 256.
 #include <cuda_fp16.h>
 
@@ -138,7 +139,13 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
   unsigned char* ring = base + warp * (R::kStages * R::kTile);
   unsigned char* scales = base + R::kOffScale + warp * (R::kStages * R::kSub * 32);
   constexpr int SUB = R::kSub;
-  constexpr int kNear = TERMS == 3 ? 2 : 8;  // binary places between the largest V scale and one for f16 weights
+  // Weights, at most 1 in the units of the largest V scale, are multiplied by
+  // 2^kUp, so that f16 holds 2^-14 .. 2^15 of them as normal numbers.  A tile with a weight that is
+  // not zero but under kLeast takes the bf16 products, whose range is fp32's:
+  // 2^-14 leaves one f16 term its 2^-11 of a weight (bf16 outputs), 2^-6 two
+  // terms 2^-19 (the second is rounded to 2^-25).
+  constexpr int kUp = 15;
+  constexpr float kLeast = TERMS == 3 ? 0x1p-6f : 0x1p-14f;
   if (lane == 0) {
     for (int s = 0; s < R::kStages; ++s) mbar_init(bars + s, 1);
     fence_barrier_init();
@@ -297,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       float acc[8][4];
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-      // e4m3: acc is held in units of 2^(e_acc - 127), the largest V scale byte
-      // of a visible token so far, so that weight * scale is at most 1
+      // e4m3: acc is held in units of 2^(e_acc - 127 - kUp), e_acc the largest V
+      // scale byte of a visible token so far: weight * scale is at most 2^kUp
       int e_acc = -1000;
 
       auto page_of = [&](int x, int j) { return __shfl_sync(0xffffffffu, (x >> 5) == j ? pages : pages1, x & 31); };
@@ -439,16 +446,11 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           }
         }
         const float r0 = m0 == ninf ? 0.f : -m0, r1 = m1 == ninf ? 0.f : -m1;  // nothing seen: exp2(-inf) = 0
-        bool near = false;  // every scale is near enough to the largest for f16 weights
         if (E4M3) {
-          int hi = -1000, lo = 1000;
+          int hi = -1000;
 #pragma unroll
-          for (int y = 0; y < SUB; ++y) {
-            hi = max(hi, max(v0[y] ? ea[y] : -1000, v1[y] ? eb[y] : -1000));
-            lo = min(lo, min(v0[y] ? ea[y] : 1000, v1[y] ? eb[y] : 1000));
-          }
+          for (int y = 0; y < SUB; ++y) hi = max(hi, max(v0[y] ? ea[y] : -1000, v1[y] ? eb[y] : -1000));
           hi = __reduce_max_sync(0xffffffffu, hi);
-          lo = __reduce_min_sync(0xffffffffu, lo);
           if (hi > e_acc) {
             const float f = e_acc < hi - 126 ? 0.f : __uint_as_float((uint32_t)(127 + e_acc - hi) << 23);
             e_acc = hi;
@@ -460,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
               acc[mt][3] *= f;
             }
           }
-          near = lo >= e_acc - kNear;
         }
 #pragma unroll
         for (int y = 0; y < SUB; ++y) {
@@ -470,18 +471,23 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
           float p2 = fast_exp2(z[y][2] + r0), p3 = fast_exp2(z[y][3] + r1);
           l0 += p0 + p2;
           l1 += p1 + p3;
-          if (E4M3) {  // times 2^(scale - e_acc); a scale byte of a hidden token may be anything
-            const float fa = v0[y] ? __uint_as_float((uint32_t)max(0, 127 + ea[y] - e_acc) << 23) : 0.f;
-            const float fb = v1[y] ? __uint_as_float((uint32_t)max(0, 127 + eb[y] - e_acc) << 23) : 0.f;
+          bool f16_holds = false;  // f16 holds every weight of the tile
+          if (E4M3) {  // times 2^(scale - e_acc + kUp); a scale byte of a hidden token may be anything
+            const float fa = v0[y] ? __uint_as_float((uint32_t)max(0, 127 + kUp + ea[y] - e_acc) << 23) : 0.f;
+            const float fb = v1[y] ? __uint_as_float((uint32_t)max(0, 127 + kUp + eb[y] - e_acc) << 23) : 0.f;
             p0 *= fa;
             p1 *= fa;
             p2 *= fb;
             p3 *= fb;
+            // (less one: a zero becomes the largest word; weights compare as their bits do)
+            const uint32_t least = min(min(__float_as_uint(p0) - 1u, __float_as_uint(p1) - 1u),
+                                       min(__float_as_uint(p2) - 1u, __float_as_uint(p3) - 1u));
+            f16_holds = !__any_sync(0xffffffffu, least < __float_as_uint(kLeast) - 1u);
           }
-          if (E4M3 && near && !edge[y]) {
-            // Weights and codes in f16.  fp32 outputs: two terms, 2^-23 of a
-            // weight or 2^-25 of the largest; bf16 outputs: one, 2^-12 (the
-            // output's own rounding is 2^-9).
+          if (E4M3 && f16_holds && !edge[y]) {
+            // Weights and codes in f16.  fp32 outputs: two terms, 2^-19 of a
+            // weight and less; bf16 outputs: one, 2^-11 (the output's own
+            // rounding is 2^-8).
             constexpr int FT = TERMS == 3 ? 2 : 1;
             uint32_t bt0[FT], bt1[FT];
 #pragma unroll
@@ -530,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
             bt1[x] = movmatrix_t(hi);
           }
           // ---- O^T += V^T P^T
-          if (E4M3) {  // as above, in bf16: for a scale far below the largest, which needs its range, and
+          if (E4M3) {  // as above, in bf16: for weights far below the largest, which need its range, and
                        // where tokens are hidden, whose codes may be NaN (here they become numbers)
             const unsigned char* vt = st + R::kBox;
             const uint4 x0 = lds128(vt + swz128(2 * c, gq)), x1 = lds128(vt + swz128(2 * c + 1, gq));
@@ -576,12 +582,14 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
 
       if (E4M3) {  // acc in its own units again
         const float f = e_acc < 0 ? 0.f : __uint_as_float((uint32_t)e_acc << 23);
+        const float down = 1.f / (float)(1 << kUp);
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-          acc[mt][0] *= f;
-          acc[mt][1] *= f;
-          acc[mt][2] *= f;
-          acc[mt][3] *= f;
+          // (in two steps: f alone spans the normal numbers)
+          acc[mt][0] = acc[mt][0] * down * f;
+          acc[mt][1] = acc[mt][1] * down * f;
+          acc[mt][2] = acc[mt][2] * down * f;
+          acc[mt][3] = acc[mt][3] * down * f;
         }
       }
 

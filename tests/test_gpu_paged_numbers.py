@@ -1,0 +1,114 @@
+"""The paged cache where numbers go to their limits: weights far below the
+largest one, against the float64 oracle and relative to the row's own size.
+
+Tolerances, from the arithmetic.  An output is sum p_t v_t, so a relative error
+w of every weight moves it by at most w * sum p_t |v_t|:
+  w: a weight's representation - one f16 or bf16 term for bf16 outputs (2^-11,
+     2^-8), two f16 terms that hold 2^-19 or three bf16 terms for fp32 outputs;
+  dz: the exponent z * log2(e) takes four roundings (log2(e), its product with
+     scale, the score, the difference to the maximum), each 2^-24 of |z| log2(e),
+     once for a weight and once for the sum; exp2 itself 2^-22;
+  steps: (N / 16 + 64) partial sums of 2^-23 each, as the products add up;
+and the output is rounded once: 2^-8 of it (bf16) or 2^-24 (fp32).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged_oracle as PO
+from test_gpu_paged import Case
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+
+
+@pytest.fixture(scope="module")
+def sa():
+    import block_sparse_kv_page_b200
+    return block_sparse_kv_page_b200
+
+
+def upload(c):
+    """The host copies of a case to its cache and queries."""
+    for host, held in ((c.k, c.dk), (c.v, c.dv)):
+        held.view(torch.uint8).copy_(host.view(torch.uint8))
+    if c.e4m3:
+        c.dks.copy_(c.ks)
+        c.dvs.copy_(c.vs)
+    c.dq.copy_(c.q)
+
+
+def check_rows(c, got, scale, zmax, decode, window=0, sinks=0):
+    """Against the oracle, relative to sum p |v|; zmax: the largest |z| in log2 units."""
+    out, ls = got
+    bf = c.out_dtype == torch.bfloat16
+    G = c.hq // c.hkv
+    for b, (N, m) in enumerate(zip(c.lens, c.rows)):
+        r0 = c.off[b]
+        for h in range(c.hkv):
+            k, v, ok = c.held(b, h)
+            q = c.q[r0:r0 + m, h * G:(h + 1) * G].double().numpy()
+            pos = np.arange(N - m, N)
+            want, wl = PO.attend_rows(q, k, v, pos, ok, window, sinks, scale)
+            size, _ = PO.attend_rows(q, k, np.abs(v), pos, ok, window, sinks, scale)
+            w = (2.0 ** -11 if decode and c.e4m3 else 2.0 ** -8) if bf else 2.0 ** -19
+            dz = 4 * zmax * 2.0 ** -24 + 2.0 ** -22
+            steps = (N / 16 + 64) * 2.0 ** -23
+            tol = (w + 2 * dz + steps) * size + (2.0 ** -8 if bf else 2.0 ** -24) * np.abs(want)
+            o = out[r0:r0 + m, h * G:(h + 1) * G].double().cpu().numpy()
+            err = np.abs(o - want)
+            assert (err <= tol).all(), (b, h, float((err / np.maximum(size, 1e-300)).max()),
+                                        np.argwhere(~(err <= tol))[:3].tolist())
+            el = np.abs(ls[r0:r0 + m, h * G:(h + 1) * G].double().cpu().numpy() - wl)
+            assert (el <= 2 * dz + steps + 2.0 ** -23 * np.abs(wl)).all(), (b, h, float(el.max()))
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("cache,spread", [("bf16", 0), ("e4m3", 0), ("e4m3", 8)])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("N,at", [(40, 5), (300, 299), (32768, 20000)])
+def test_one_dominant_token_without_a_value(cuda_dev, sa, cache, out, decode, spread, N, at):
+    """One token has all but 2^-gap of the weight and a value of zero, as
+    attention sinks have: the output is what the others give, each of them gap
+    bits below the largest weight.  spread: every other V row is held with a
+    scale that many places smaller."""
+    c = Case(sa, cuda_dev, lens=[N], rows=[1], hq=8, hkv=2, page=16, cache=cache, out=out, seed=201)
+    c.q.zero_()
+    c.q[:, :, 3] = 1
+    page, slot = int(c.table[0, at // 16]), at % 16
+    k, v = torch.zeros_like(c.k.float()), c.v.float().abs().clamp(min=2.0 ** -5)
+    k[page, :, slot, 3] = 1
+    v[page, :, slot] = 0
+    c.k, c.v = k.to(c.k.dtype), v.to(c.v.dtype)
+    if c.e4m3:
+        c.ks.fill_(127)
+        c.vs.fill_(127)
+        c.vs[:, :, 1::2] -= spread
+    upload(c)
+    for gap in (12, 20, 24.5, 28, 33.25, 60):
+        scale = float(np.float32(gap * math.log(2)))
+        check_rows(c, c.run(decode=decode, scale=scale), scale, gap, decode)
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("louder", [10, 16, 40])
+def test_a_loud_value_that_is_hardly_seen(cuda_dev, sa, out, decode, louder):
+    """One V row whose scale is 2^louder times the others' and whose weight is
+    2^-60 of theirs."""
+    c = Case(sa, cuda_dev, lens=[700], rows=[1], hq=8, hkv=2, page=16, cache="e4m3", out=out, seed=202)
+    c.q.zero_()
+    c.q[:, :, 3] = 1
+    k, v = torch.zeros_like(c.k.float()), c.v.float().abs().clamp(min=2.0 ** -5)
+    page, slot = int(c.table[0, 2]), 7
+    k[page, :, slot, 3] = -1
+    c.k, c.v = k.to(c.k.dtype), v.to(c.v.dtype)
+    c.ks.fill_(127)
+    c.vs.fill_(120)
+    c.vs[page, :, slot] += louder
+    upload(c)
+    scale = float(np.float32(60 * math.log(2)))
+    check_rows(c, c.run(decode=decode, scale=scale), scale, 60, decode)
