@@ -154,6 +154,7 @@ sa_status decode(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   const PagedView& kv = p.kv;
   a.p = p;
   a.scale_log2 = p.scale * kLog2e;
+  a.scale_frac = std::frexp(a.scale_log2, &a.scale_exp);
   if (!cache_maps(kv, &a.tmap_k, &a.tmap_v, 16)) return SA_ERR_CUDA;
   const int grid = paged_decode_grid(device_sm_count());
   const long long units = (long long)kv.B * kv.Hkv;

@@ -88,7 +88,9 @@ int chunk_block_tokens();
 struct PagedDecodeArgs {
   CUtensorMap tmap_k, tmap_v;        // [n_pages][Hkv][page_size][128], box 1 x 1 x 16 x 128 bytes, 128B swizzle
   PagedAttnArgs p;                   // row b of sequence b
-  float scale_log2;                  // scale * log2(e)
+  float scale_log2;                  // scale * log2(e) = scale_frac * 2^scale_exp, |scale_frac| < 1
+  float scale_frac;
+  int scale_exp;
   int by_unit;                       // recs by unit (b * Hkv + g) instead of by CTA
   float* parts;                      // [grid][head, tail segment][8 heads][132]
   int4* recs;                        // cut units: first CTA (-1: none), last CTA, b, g

@@ -32,7 +32,7 @@
 // relative to the largest scale seen, which is followed like the maximum; tiles
 // with a weight below what f16 holds take the same products in bf16 (whose
 // conversion, by shifts and masks, costs three times as much: 16 sequences of
-// 32k tokens 183 us, 220 where every tile takes it).  The rows' scales (powers of two)
+// 32k tokens 185 us, 222 where every tile takes it).  The rows' scales (powers of two)
 // multiply the scores and the weights, 4 values a lane instead of 256.
 #include <cuda_fp16.h>
 
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       const __nv_bfloat16* qrow =
           a.p.q + (size_t)b * a.p.q_row_stride + (size_t)(g * G + (head_ok ? gq : 0)) * kHeadDim;
       uint32_t bq[16];
-      float q_scale = 1.f;  // of head gq: its values are q * q_scale here
+      int q_exp = 0;  // of head gq: its values are q * 2^-q_exp here
       if (E4M3) {
         // f16, as the codes become: each head's values times the power of two
         // that brings the largest below 2^14 (f16 holds them exactly, those
@@ -281,18 +281,31 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
         mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
         mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
         const int e = min(253, max(1, 127 + 13 - ((int)(__float_as_uint(mq) >> 23) - 127)));
-        q_scale = __uint_as_float((uint32_t)e << 23);
+        const float up = __uint_as_float((uint32_t)e << 23);
+        q_exp = 127 - e;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t y[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) bq[4 * s + i] = pack_f16(bf16_lo(y[i]) * q_scale, bf16_hi(y[i]) * q_scale);
+          for (int i = 0; i < 4; ++i) bq[4 * s + i] = pack_f16(bf16_lo(y[i]) * up, bf16_hi(y[i]) * up);
         }
-        q_scale = __uint_as_float((uint32_t)(254 - e) << 23);  // its inverse
       }
-      // scores of heads 2 c, 2 c + 1 are multiplied by
-      const float zs0 = a.scale_log2 * __shfl_sync(0xffffffffu, q_scale, 8 * c);
-      const float zs1 = a.scale_log2 * __shfl_sync(0xffffffffu, q_scale, 8 * c + 4);
+      // Sums of heads 2 c, 2 c + 1 times zs, times the row's scale (e4m3), times
+      // zu are scores.  A sum is below 2^30 in e4m3, so with zs within 2^-60 ..
+      // 2^90 no product on the way overflows, or loses bits, where the score
+      // does not; what scale and 2^q_exp leave for zu is 1 but for queries or
+      // scales near the ends of fp32.  (Above 2^127, both past 2^100, it is
+      // capped: only lse shows it, scores are 2^60 apart there.)
+      float zs0 = a.scale_log2, zs1 = a.scale_log2, zu0 = 1.f, zu1 = 1.f;
+      if (E4M3) {
+        auto split = [&](int q, float& zs, float& zu) {
+          const int e = a.scale_exp + q, in = min(max(e, -60), 90);
+          zs = a.scale_frac * __uint_as_float((uint32_t)(127 + in) << 23);
+          zu = __uint_as_float((uint32_t)(127 + min(max(e - in, -126), 127)) << 23);
+        };
+        split(__shfl_sync(0xffffffffu, q_exp, 8 * c), zs0, zu0);
+        split(__shfl_sync(0xffffffffu, q_exp, 8 * c + 4), zs1, zu1);
+      }
       if (!E4M3) {  // step s: dims 16 s + 2 c (+ 1), 16 s + 8 + 2 c (+ 1)
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
@@ -416,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
               mma_bf16(k & 1 ? s2 : s, a0, a1, a2, a3, bq[2 * k], bq[2 * k + 1]);
             }
           }
-          // tokens gq / gq + 8, heads 2 c / 2 c + 1; q's scale first: sums of scaled
-          // values times a huge key scale would overflow where the score does not
+          // tokens gq / gq + 8, heads 2 c / 2 c + 1
           z[y][0] = v0[y] ? (s[0] + s2[0]) * zs0 * ka : ninf;
           z[y][1] = v0[y] ? (s[1] + s2[1]) * zs1 * ka : ninf;
           z[y][2] = v1[y] ? (s[2] + s2[2]) * zs0 * kb : ninf;
@@ -429,6 +441,10 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
         for (int o = 4; o < 32; o <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        }
+        if (E4M3) {
+          mx0 *= zu0;
+          mx1 *= zu1;
         }
         const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
         if (__any_sync(0xffffffffu, mn0 > m0 || mn1 > m1)) {
@@ -467,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
         for (int y = 0; y < SUB; ++y) {
           if (!good[y]) continue;
           unsigned char* st = ring + s_it * R::kTile + y * (R::kTile / SUB);
-          float p0 = fast_exp2(z[y][0] + r0), p1 = fast_exp2(z[y][1] + r1);
-          float p2 = fast_exp2(z[y][2] + r0), p3 = fast_exp2(z[y][3] + r1);
+          float p0 = fast_exp2(fmaf(z[y][0], zu0, r0)), p1 = fast_exp2(fmaf(z[y][1], zu1, r1));
+          float p2 = fast_exp2(fmaf(z[y][2], zu0, r0)), p3 = fast_exp2(fmaf(z[y][3], zu1, r1));
           l0 += p0 + p2;
           l1 += p1 + p3;
           bool f16_holds = false;  // f16 holds every weight of the tile

@@ -112,3 +112,31 @@ def test_a_loud_value_that_is_hardly_seen(cuda_dev, sa, out, decode, louder):
     upload(c)
     scale = float(np.float32(60 * math.log(2)))
     check_rows(c, c.run(decode=decode, scale=scale), scale, 60, decode)
+
+
+# Powers of two of the queries, of the keys and of the scale; the scores are
+# those of (0, 0, 0): huge queries and tiny keys, the other way round, a huge
+# and a tiny scale.  (Sums of query times key stay within fp32 in all of them.)
+POWERS = [(112, -124, 12), (122, -124, 2), (-100, 110, -10), (-124, 117, 7), (0, -124, 124), (-20, -100, 120),
+          (60, 50, -110), (0, 112, -112), (0, 0, 0)]
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("q_power,k_power,s_power", POWERS)
+def test_ordinary_scores_from_factors_far_apart(cuda_dev, sa, out, decode, q_power, k_power, s_power):
+    """Query, key scale and scale of the scores at the ends of their range,
+    where partial products in another order pass what fp32 holds; scores to
+    about 40."""
+    c = Case(sa, cuda_dev, lens=[700, 40], rows=[1, 1] if decode else [9, 2], hq=8, hkv=2, page=16, cache="e4m3",
+             out=out, seed=203)
+    g = torch.Generator().manual_seed(1)
+    c.q = (c.q.float().abs().clamp(0.25, 1.75) * 2.0 ** q_power).to(torch.bfloat16)
+    sign = torch.where(torch.rand((*c.k.shape[:3], 1), generator=g) < 0.5, -1.0, 1.0)
+    c.k = (c.k.float().abs() * sign).to(c.k.dtype)   # (a token's products have one sign)
+    c.ks.copy_(torch.randint(127, 130, c.ks.shape, generator=g) + k_power)
+    upload(c)
+    scale = 0.003 * 2.0 ** s_power
+    scale = float(np.float32(scale))
+    c.check(c.run(decode=decode, scale=scale), scale=scale)
+    c.check(c.run(30, 3, decode=decode, scale=scale), 30, 3, scale=scale)
