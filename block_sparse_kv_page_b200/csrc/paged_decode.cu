@@ -32,9 +32,11 @@
 // relative to the largest scale seen, which is followed like the maximum; tiles
 // with a weight below what f16 holds take the same products in bf16 (whose
 // conversion, by shifts and masks, costs three times as much: 16 sequences of
-// 32k tokens 185 us, 222 where every tile takes it).  The rows' scales (powers of two)
+// 32k tokens 188 us, 224 where every tile takes it).  The rows' scales (powers of two)
 // multiply the scores and the weights, 4 values a lane instead of 256.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "paged.cuh"
 #include "internal.h"
@@ -263,24 +265,30 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
       const __nv_bfloat16* qrow =
           a.p.q + (size_t)b * a.p.q_row_stride + (size_t)(g * G + (head_ok ? gq : 0)) * kHeadDim;
       uint32_t bq[16];
-      int q_exp = 0;  // of head gq: its values are q * 2^-q_exp here
+      int q_exp = 0;      // of head gq: its values are q * 2^-q_exp here
+      bool wide = false;  // f16 does not hold some head's values
       if (E4M3) {
         // f16, as the codes become: each head's values times the power of two
-        // that brings the largest below 2^14 (f16 holds them exactly, those
-        // under 2^-28 of the largest to 2^-38 of it).  Step s: dims 32 c + 4 s
-        // + {0, 1} and {2, 3}.
+        // that brings the largest below 2^14.  Step s: dims 32 c + 4 s + {0, 1}
+        // and {2, 3}.  f16 holds all but those under 2^-31 of the largest; where
+        // it does not hold one exactly, keys and queries go to bf16, the largest
+        // brought below 2^111 (sums stay below 2^127), in the order {0, 2}, {1, 3}.
         uint4 x[4];
-        float mq = 0.f;
+        uint32_t top = 0u, low = 0xffffffffu;  // of two values each: the largest |q|, the smallest but 0, as bits
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           x[s] = head_ok ? ldg_nc128(qrow + 32 * c + 8 * s) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t y[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mq = fmaxf(mq, fmaxf(fabsf(bf16_lo(y[i])), fabsf(bf16_hi(y[i]))));
+          for (int i = 0; i < 4; ++i) {
+            top = __vmaxu2(top, y[i] & 0x7fff7fffu);
+            low = __vminu2(low, __vsub2(y[i] & 0x7fff7fffu, 0x00010001u));  // (less one: 0 becomes the largest)
+          }
         }
-        mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
-        mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
-        const int e = min(253, max(1, 127 + 13 - ((int)(__float_as_uint(mq) >> 23) - 127)));
+        int mq = max(top & 0xffffu, top >> 16);
+        mq = max(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
+        mq = max(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
+        const int e = min(253, max(1, 127 + 13 - ((mq >> 7) - 127)));
         const float up = __uint_as_float((uint32_t)e << 23);
         q_exp = 127 - e;
 #pragma unroll
@@ -289,17 +297,34 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
 #pragma unroll
           for (int i = 0; i < 4; ++i) bq[4 * s + i] = pack_f16(bf16_lo(y[i]) * up, bf16_hi(y[i]) * up);
         }
+        // 8 bits of a value from 2^-17 on reach f16's last place, 2^-24
+        const bool exact = (int)min(low & 0xffffu, low >> 16) >= ((127 - 17 + 127 - e) << 7) - 1;
+        wide = __any_sync(0xffffffffu, !exact);
+        if (wide) {
+          const int ew = min(253, max(1, 127 + 110 - ((mq >> 7) - 127)));
+          const float upw = __uint_as_float((uint32_t)ew << 23);
+          q_exp = 127 - ew;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t y[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              bq[4 * s + i] = pack_bf16(bf16_lo(y[i]) * upw, bf16_lo(y[i + 1]) * upw);
+              bq[4 * s + i + 1] = pack_bf16(bf16_hi(y[i]) * upw, bf16_hi(y[i + 1]) * upw);
+            }
+          }
+        }
       }
       // Sums of heads 2 c, 2 c + 1 times zs, times the row's scale (e4m3), times
-      // zu are scores.  A sum is below 2^30 in e4m3, so with zs within 2^-60 ..
-      // 2^90 no product on the way overflows, or loses bits, where the score
+      // zu are scores.  A sum is below 2^30 in e4m3 (2^127 if wide), so with zs
+      // within 2^-60 .. 2^90 (2^-120 .. 1) no product on the way overflows, or loses bits, where the score
       // does not; what scale and 2^q_exp leave for zu is 1 but for queries or
       // scales near the ends of fp32.  (Above 2^127, both past 2^100, it is
       // capped: only lse shows it, scores are 2^60 apart there.)
       float zs0 = a.scale_log2, zs1 = a.scale_log2, zu0 = 1.f, zu1 = 1.f;
       if (E4M3) {
         auto split = [&](int q, float& zs, float& zu) {
-          const int e = a.scale_exp + q, in = min(max(e, -60), 90);
+          const int e = a.scale_exp + q, in = min(max(e, wide ? -120 : -60), wide ? 0 : 90);
           zs = a.scale_frac * __uint_as_float((uint32_t)(127 + in) << 23);
           zu = __uint_as_float((uint32_t)(127 + min(max(e - in, -126), 127)) << 23);
         };
@@ -401,8 +426,57 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
               __syncwarp();
             }
           }
-          // ---- S^T = K Q^T, two chains (a tile that was not loaded gives junk, which nothing sees)
-          float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+        }
+        // ---- S^T = K Q^T, two chains a tile (a tile that was not loaded gives junk, which nothing sees)
+        float s[SUB][4], s2[SUB][4];
+#pragma unroll
+        for (int y = 0; y < SUB; ++y)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[y][x] = s2[y][x] = 0.f;
+        if (E4M3) {
+          auto products = [&](auto f16) {
+#pragma unroll
+            for (int y = 0; y < SUB; ++y) {
+              const unsigned char* st = ring + s_it * R::kTile + y * (R::kTile / SUB);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint4 xk = lds128(st + swz128(gq, 2 * c + h)), yk = lds128(st + swz128(gq + 8, 2 * c + h));
+                const uint32_t xs[4] = {xk.x, xk.y, xk.z, xk.w}, ys[4] = {yk.x, yk.y, yk.z, yk.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int k = 4 * h + i;
+                  if (f16)
+                    mma_f16(i & 1 ? s2[y] : s[y], f16_of_codes(xs[i], false), f16_of_codes(ys[i], false),
+                            f16_of_codes(xs[i], true), f16_of_codes(ys[i], true), bq[2 * k], bq[2 * k + 1]);
+                  else
+                    mma_bf16(i & 1 ? s2[y] : s[y], bf16_low_codes(xs[i]), bf16_low_codes(ys[i]),
+                             bf16_high_codes(xs[i]), bf16_high_codes(ys[i]), bq[2 * k], bq[2 * k + 1]);
+                }
+              }
+            }
+          };
+          products(std::true_type{});
+          if (wide) {  // (again: a choice between the two, ahead of them, cost the usual path 2%)
+#pragma unroll
+            for (int y = 0; y < SUB; ++y)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) s[y][x] = s2[y][x] = 0.f;
+            products(std::false_type{});
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < SUB; ++y) {
+            const unsigned char* st = ring + s_it * R::kTile + y * (R::kTile / SUB);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint32_t a0, a1, a2, a3;
+              ldsm_x4(a0, a1, a2, a3, st + (k >> 2) * R::kBox + swz128(lrow_a, 2 * (k & 3) + lchk_a));
+              mma_bf16(k & 1 ? s2[y] : s[y], a0, a1, a2, a3, bq[2 * k], bq[2 * k + 1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < SUB; ++y) {
           float ka = 1.f, kb = 1.f;  // the tokens' scales
           if (E4M3) {
             const unsigned char* sc = scales + (s_it * SUB + y) * 32;
@@ -410,30 +484,12 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
             kb = __uint_as_float((uint32_t)sc[gq + 8] << 23);
             ea[y] = sc[16 + gq];
             eb[y] = sc[16 + gq + 8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 xk = lds128(st + swz128(gq, 2 * c + h)), yk = lds128(st + swz128(gq + 8, 2 * c + h));
-              const uint32_t xs[4] = {xk.x, xk.y, xk.z, xk.w}, ys[4] = {yk.x, yk.y, yk.z, yk.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int k = 4 * h + i;
-                mma_f16(i & 1 ? s2 : s, f16_of_codes(xs[i], false), f16_of_codes(ys[i], false),
-                        f16_of_codes(xs[i], true), f16_of_codes(ys[i], true), bq[2 * k], bq[2 * k + 1]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint32_t a0, a1, a2, a3;
-              ldsm_x4(a0, a1, a2, a3, st + (k >> 2) * R::kBox + swz128(lrow_a, 2 * (k & 3) + lchk_a));
-              mma_bf16(k & 1 ? s2 : s, a0, a1, a2, a3, bq[2 * k], bq[2 * k + 1]);
-            }
           }
           // tokens gq / gq + 8, heads 2 c / 2 c + 1
-          z[y][0] = v0[y] ? (s[0] + s2[0]) * zs0 * ka : ninf;
-          z[y][1] = v0[y] ? (s[1] + s2[1]) * zs1 * ka : ninf;
-          z[y][2] = v1[y] ? (s[2] + s2[2]) * zs0 * kb : ninf;
-          z[y][3] = v1[y] ? (s[3] + s2[3]) * zs1 * kb : ninf;
+          z[y][0] = v0[y] ? (s[y][0] + s2[y][0]) * zs0 * ka : ninf;
+          z[y][1] = v0[y] ? (s[y][1] + s2[y][1]) * zs1 * ka : ninf;
+          z[y][2] = v1[y] ? (s[y][2] + s2[y][2]) * zs0 * kb : ninf;
+          z[y][3] = v1[y] ? (s[y][3] + s2[y][3]) * zs1 * kb : ninf;
           mx0 = fmaxf(mx0, fmaxf(z[y][0], z[y][2]));
           mx1 = fmaxf(mx1, fmaxf(z[y][1], z[y][3]));
         }

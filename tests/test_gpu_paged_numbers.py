@@ -140,3 +140,24 @@ def test_ordinary_scores_from_factors_far_apart(cuda_dev, sa, out, decode, q_pow
     scale = float(np.float32(scale))
     c.check(c.run(decode=decode, scale=scale), scale=scale)
     c.check(c.run(30, 3, decode=decode, scale=scale), 30, 3, scale=scale)
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("power", [20, 31, 45, 127, -100])
+def test_one_query_dim_far_above_the_others(cuda_dev, sa, out, decode, power):
+    """One dim of some heads' queries is 2^power (or all others 2^power), where
+    the keys are zero: the other dims make the scores."""
+    c = Case(sa, cuda_dev, lens=[700, 40], rows=[1, 1] if decode else [9, 2], hq=8, hkv=2, page=16, cache="e4m3",
+             out=out, seed=204)
+    scale = 1 / math.sqrt(D)
+    c.q[:, ::3, 77] = 2.0 ** max(power, 0)
+    if power < 0:
+        c.q = torch.where(torch.arange(D) == 77, c.q.float(), c.q.float() * 2.0 ** power).to(torch.bfloat16)
+        scale *= 2.0 ** -power
+    k = c.k.float()
+    k[..., 77] = 0
+    c.k = k.to(c.k.dtype)
+    upload(c)
+    c.check(c.run(decode=decode, scale=scale), scale=scale)
+    c.check(c.run(30, 3, decode=decode, scale=scale), 30, 3, scale=scale)
