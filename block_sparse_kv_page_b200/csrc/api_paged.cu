@@ -46,7 +46,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Scratch of the attention calls, from kScratch on.
 struct PagedScratch {
-  size_t parts, xbuf, recs, total;
+  size_t parts, xbuf, recs, odd, total;
 };
 PagedScratch paged_scratch() {
   const size_t sms = (size_t)device_sm_count();
@@ -54,7 +54,8 @@ PagedScratch paged_scratch() {
   s.parts = kScratch;
   s.xbuf = s.parts + align256(sms * 2 * 2 * kChunkPart * sizeof(float));
   s.recs = s.xbuf + align256(sms * kChunkPart * sizeof(float));
-  s.total = s.recs + align256(sms * sizeof(ChunkRec));
+  s.odd = s.recs + align256(sms * sizeof(ChunkRec));
+  s.total = s.odd + align256(sms * sizeof(ChunkOdd));
   // (the decode's parts and records, smaller, lie in the same place)
   return s;
 }
@@ -184,6 +185,7 @@ sa_status chunk(const PagedAttnArgs& p, unsigned char* ws, cudaStream_t st) {
   a.parts = (float*)(ws + sc.parts);
   a.xbuf = (float*)(ws + sc.xbuf);
   a.recs = (ChunkRec*)(ws + sc.recs);
+  a.odd = (ChunkOdd*)(ws + sc.odd);
   return launched(launch_chunk(a, device_sm_count(), st));
 }
 

@@ -59,6 +59,16 @@
 // Roles run ahead of each other over block and segment boundaries; only the
 // mbarriers order them.
 //
+// A weight of 0 keeps no NaN or infinity of a V row out of the products.  Rows
+// that no row of the pair sees are zeros by the time of PV.  In rows that some
+// see and others do not such a value makes its dim NaN in every vector of the
+// tile; so a look at the first vector's result shows it.  combine_kernel then
+// looks through those V rows, and takes the dims that have such a value again,
+// token by token.  (A bf16 cache only: what the converters write are numbers.
+// Four bf16 prompts 127 -> 129.5 us, 16 rows over 29.5k tokens 43.8 -> 46.4;
+// looking through the V rows ahead of PV cost the prompts 1 to 38 us and the
+// short calls 2 to 6, by whichever warps.)
+//
 // P is rounded to bf16 where the output is bf16 (its error, 2^-9 per weight, is
 // that of the output's own rounding); for fp32 outputs it is split into three
 // bf16 terms (24 bits), which leaves room for one S buffer per slot.
@@ -494,7 +504,10 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
   }
   grid_dep_wait();
   make_plan(a, &s_plan, s_scan);
-  if (tid == 0) a.recs[blockIdx.x] = ChunkRec{0, 0, 0, 0, 0};
+  if (tid == 0) {
+    a.recs[blockIdx.x] = ChunkRec{0, 0, 0, 0, 0};
+    if (!E4M3) a.odd[blockIdx.x] = ChunkOdd{0x7fffffff, -1};
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -962,6 +975,7 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
       const bool mine = vok && !dead && !(sg.single && t == 1 && sg.nb == 0);  // (then slot 0 writes the zeros)
       f0 *= inv;
       f1 *= inv;
+      float odd = 0.f;  // lanes that have some of vector 0: NaN if it has a result that is no number
       if (!part && !other) {
         // The usual end: straight to the output.  With a thread per row each
         // store instruction touches 32 lines; here lanes take 16 rows x 8 columns
@@ -990,6 +1004,9 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
               o[2 * n] = __uint_as_float(q[4 * n + 2 * y]) * f;
               o[2 * n + 1] = __uint_as_float(q[4 * n + 2 * y + 1]) * f;
             }
+            if (!E4M3 && y == 0 && !(c & 1) && quarter == 0 && lane < 4)
+#pragma unroll
+              for (int n = 0; n < 8; ++n) odd = fmaf(o[n], 0.f, odd);
             const int d0 = 64 * half + 32 * (c >> 1);
             if (a.p.out) {
               float* d = a.p.out + ro * kHeadDim + d0 + 2 * (lane & 3);
@@ -1048,6 +1065,9 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
             o[4 * x + 3] += y[x].w * f1;
           }
         }
+        if (!E4M3 && r == 0)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) odd = fmaf(o[x], 0.f, odd);
         if (mine) {
           if (part) {
 #pragma unroll
@@ -1073,6 +1093,10 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
         else if (a.p.lse) a.p.lse[orow] = lh != 0.f ? mref * kLn2 + logf(lh) : ninf;
         if (sg.i0 == 0 && qpos < 0) flag_status(status, SA_ERR_DEVICE_CHECK);
       }
+      if (!E4M3 && odd != 0.f) {
+        atomicMin(&a.odd[blockIdx.x].from, sg.b);
+        atomicMax(&a.odd[blockIdx.x].to, sg.b);
+      }
       if (merge) {
         __threadfence_block();
         __syncwarp();
@@ -1092,16 +1116,141 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
+// What follows is for a bf16 cache with values that are no numbers in V rows that
+// some rows of a pair see and others do not.
+
+// Whether there are such values, in the dims that this lane has (a warp, 4 dims a lane).
+SA_DEV bool odd_values(const ChunkArgs& a, int b, int g, const Geom& q) {
+  const PagedView& kv = a.p.kv;
+  const int before = a.p.window ? max(q.p1 - a.p.window + 1 - q.lo, 0) : 0, all = before + q.rows - 1;
+  bool odd = false;
+  for (int x = 0; x < all; ++x) {
+    const int t = x < before ? q.lo + x : q.p0 + 1 + x - before;
+    if (t < 0) continue;
+    const int e = t / kv.page_size, page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
+    if (page < 0 || page >= kv.n_pages) continue;
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(kv.v + paged_offset(kv, page, g, t - e * kv.page_size)) +
+                          (threadIdx.x & 31));
+    const uint32_t x0 = (w.x & 0x7f807f80u) + 0x00800080u, x1 = (w.y & 0x7f807f80u) + 0x00800080u;
+    odd |= ((x0 | x1) & 0x80008000u) != 0u;  // a half with an exponent of 255
+  }
+  return odd;
+}
+
+// Row `row` of sequence b at position p, query head h, token by token: a warp, 4 dims a lane.
+SA_DEV float4 again_vector(const ChunkArgs& a, int b, int row, int p, int h) {
+  const PagedView& kv = a.p.kv;
+  const int lane = threadIdx.x & 31, g = h / a.p.G;
+  const float ninf = -__int_as_float(0x7f800000);
+  const uint2 qw = *reinterpret_cast<const uint2*>(a.p.q + (size_t)row * a.p.q_row_stride + (size_t)h * kHeadDim + 4 * lane);
+  const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
+  const int lo = a.p.window && p >= a.p.window ? p - a.p.window + 1 : 0, first = min(a.p.window ? a.p.sinks : 0, lo);
+  float m = ninf, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x = 0; x < first + p + 1 - lo; ++x) {
+    const int t = x < first ? x : lo + x - first, e = t / kv.page_size;
+    const int page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
+    if (page < 0 || page >= kv.n_pages) continue;
+    const long long at = paged_offset(kv, page, g, t - e * kv.page_size) + 8 * lane;
+    const uint2 k = __ldg(reinterpret_cast<const uint2*>(kv.k + at)), v = __ldg(reinterpret_cast<const uint2*>(kv.v + at));
+    float z = q[0] * bf16_lo(k.x) + q[1] * bf16_hi(k.x) + q[2] * bf16_lo(k.y) + q[3] * bf16_hi(k.y);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
+    z *= a.scale_log2;
+    const float mn = fmaxf(m, z), f = mn == ninf ? 1.f : fast_exp2(m - mn);
+    const float w = z == ninf ? 0.f : fast_exp2(z - mn);
+    m = mn;
+    l = l * f + w;
+    o.x = o.x * f + w * bf16_lo(v.x);
+    o.y = o.y * f + w * bf16_hi(v.x);
+    o.z = o.z * f + w * bf16_lo(v.y);
+    o.w = o.w * f + w * bf16_hi(v.y);
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+// The 8 dims from 4 d4 of a lane's vector - row `row` of a cut pair, query head h -
+// where the merge of its parts gave some that are no numbers (a warp).
+struct Dims8 {
+  float4 o[2];
+};
+__device__ __noinline__ Dims8 again_parts(const ChunkArgs& a, int row0, int g, int row, int h, bool ok, int d4,
+                                          Dims8 was) {
+  int b = 0, r0 = 0, m = 0;
+  for (; b < a.p.kv.B; ++b) {  // the sequence that has the row
+    m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, nullptr);
+    if (row0 >= r0 && row0 - r0 < m) break;
+  }
+  if (b == a.p.kv.B) return was;
+  const int N = paged_tokens(a.p.kv, b, nullptr);
+  const bool odd = odd_values(a, b, g, pair_geom(a, N, m, (row0 - r0) / (2 * a.R)));
+  const unsigned dims = __ballot_sync(0xffffffffu, odd) & (3u << d4);
+  if (!dims) return was;
+  for (unsigned todo = __ballot_sync(0xffffffffu, ok); todo; todo &= todo - 1) {
+    const int from = __ffs(todo) - 1;
+    const int i = row0 - r0 + __shfl_sync(0xffffffffu, row, from);
+    const float4 y = again_vector(a, b, r0 + i, N - m + i, __shfl_sync(0xffffffffu, h, from));
+    for (int x = 0; x < 2; ++x) {
+      const float4 mine = make_float4(__shfl_sync(0xffffffffu, y.x, d4 + x), __shfl_sync(0xffffffffu, y.y, d4 + x),
+                                      __shfl_sync(0xffffffffu, y.z, d4 + x), __shfl_sync(0xffffffffu, y.w, d4 + x));
+      if ((threadIdx.x & 31) == from && (dims >> (d4 + x) & 1u)) was.o[x] = mine;
+    }
+  }
+  return was;
+}
+
+// Rows of the pairs that were not cut, of the sequences that CTAs met results in
+// that are no numbers (the whole grid, a warp at a time).
+__device__ __noinline__ void again_rows(const ChunkArgs& a, int ctas) {
+  const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
+  const int first = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  for (int b = 0; b < a.p.kv.B; ++b) {
+    int r0;
+    const int m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, nullptr), N = paged_tokens(a.p.kv, b, nullptr);
+    bool met = false;
+    for (int c = lane; c < ctas; c += 32) met |= a.odd[c].from <= b && b <= a.odd[c].to;
+    if (m <= 0 || !__any_sync(0xffffffffu, met)) continue;
+    for (long long x = first; x < (long long)m * a.p.Hq; x += warps) {
+      const int i = (int)(x / a.p.Hq), h = (int)(x - (long long)i * a.p.Hq), g = h / a.p.G, j = i / (2 * a.R);
+      const size_t at = ((size_t)(r0 + i) * a.p.Hq + h) * kHeadDim + 4 * lane;
+      float4 o;
+      if (a.p.out) {
+        o = *reinterpret_cast<const float4*>(a.p.out + at);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(a.p.out_bf16 + at);
+        o = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+      }
+      if (!__any_sync(0xffffffffu, o.x * 0.f + o.y * 0.f + o.z * 0.f + o.w * 0.f != 0.f)) continue;
+      bool cut = false;
+      for (int c = lane; c < ctas; c += 32) cut |= a.recs[c].rows > 0 && a.recs[c].row0 == r0 + 2 * a.R * j && a.recs[c].g == g;
+      if (__any_sync(0xffffffffu, cut)) continue;  // again_parts
+      const bool odd = odd_values(a, b, g, pair_geom(a, N, m, j));
+      if (!__any_sync(0xffffffffu, odd)) continue;
+      o = again_vector(a, b, r0 + i, N - m + i, h);
+      if (!odd) continue;  // (the other dims stay as they are)
+      if (a.p.out)
+        *reinterpret_cast<float4*>(a.p.out + at) = o;
+      else
+        *reinterpret_cast<uint2*>(a.p.out_bf16 + at) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    }
+  }
+}
+
 // Merge of the partial results of the pairs that were cut: a warp's task is 32
 // vectors (one per lane) and 8 dims of the pair that one CTA began, its parts in
 // CTA order.  Tasks go round the grid, so that the few pairs of a short chunk
 // over a long cache, in many parts each, use every SM.
 constexpr int kCombineThreads = 256;
+template <bool E4M3>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ ChunkArgs a, int ctas) {
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float ninf = -__int_as_float(0x7f800000);
   const int G = a.p.G, R = a.R;
+  bool met = false;  // rare: results that are no numbers
+  if (!E4M3)
+    for (int c = threadIdx.x; c < ctas; c += kCombineThreads) met |= a.odd[c].from <= a.odd[c].to;
   const int stride = gridDim.x * (kCombineThreads / 32);
   for (int task = warp * gridDim.x + blockIdx.x; task < ctas * 128; task += stride) {
     const int c0 = task >> 7;
@@ -1152,10 +1301,19 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
       }
       M = nm;
     }
-    if (!ok) continue;
     const float inv = L != 0.f ? 1.f / L : 0.f;
+    float odd = 0.f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) o[x] = make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
+    for (int x = 0; x < 2; ++x) {
+      o[x] = make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
+      odd += o[x].x * 0.f + o[x].y * 0.f + o[x].z * 0.f + o[x].w * 0.f;
+    }
+    if (!E4M3 && __any_sync(0xffffffffu, odd != 0.f)) {
+      const Dims8 y = again_parts(a, rec.row0, rec.g, row, rec.g * G + r - rr * G, ok, d4, Dims8{{o[0], o[1]}});
+      o[0] = y.o[0];
+      o[1] = y.o[1];
+    }
+    if (!ok) continue;
     const size_t orow = (size_t)(rec.row0 + row) * a.p.Hq + (size_t)rec.g * G + (r - rr * G);
     if (a.p.out) {
       float4* d = reinterpret_cast<float4*>(a.p.out + orow * kHeadDim) + d4;
@@ -1167,6 +1325,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     }
     if (a.p.lse && d4 == 0) a.p.lse[orow] = L != 0.f ? M * kLn2 + logf(L) : ninf;
   }
+  if (!E4M3 && __syncthreads_or(met)) again_rows(a, ctas);
 }
 
 template <bool E4M3, int TERMS>
@@ -1194,7 +1353,8 @@ cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st) {
   const cudaError_t e = a.p.kv.e4m3 ? (f32 ? launch<true, 3>(a, grid, st) : launch<true, 1>(a, grid, st))
                                     : (f32 ? launch<false, 3>(a, grid, st) : launch<false, 1>(a, grid, st));
   if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel, (unsigned)grid * 4, kCombineThreads, 0, st, a, grid);
+  return launch_pdl(a.p.kv.e4m3 ? combine_kernel<true> : combine_kernel<false>, (unsigned)grid * 4, kCombineThreads, 0, st, a,
+                    grid);
 }
 
 }  // namespace sa

@@ -51,11 +51,6 @@ SA_DEV size_t scale_index(const PagedView& kv, int page, int head, int slot) {
   return ((size_t)page * kv.Hkv + head) * kv.page_size + slot;
 }
 
-// Whether the row at position p sees token t.
-SA_DEV bool row_sees(int p, int t, int window, int sinks) {
-  return t <= p && (window == 0 || t > p - window || t < sinks);
-}
-
 // The exponent of a row's scale: the smallest k with amax <= 448 * 2^k,
 // 448 = 1.75 * 2^8, from amax's own exponent and mantissa (so no rounding can
 // put it one off); clipped so that 2^k, 2^-k and every code * 2^k stay normal

@@ -70,6 +70,9 @@ constexpr int kChunkMl = 128 * 128, kChunkPart = kChunkMl + 2 * 128;
 struct ChunkRec {                    // a pair cut between CTAs, kept by the CTA that holds its first block
   int row0, rows, g, last, single;   // rows 0: none; last: the CTA that holds its last block
 };
+struct ChunkOdd {                    // sequences from .. to of which a CTA met results that are no numbers
+  int from, to;                      // from > to: none
+};
 struct ChunkArgs {
   CUtensorMap tmap_q;                // [n_rows][Hq][128], box R x G x 64, 128B swizzle
   CUtensorMap tmap_k, tmap_v;        // [n_pages][Hkv][page_size][128], box 1 x 1 x hb x 64 (bf16, 128B
@@ -81,6 +84,7 @@ struct ChunkArgs {
   float* parts;                      // [grid][head, tail segment][slot][kChunkPart]
   float* xbuf;                       // [grid][kChunkPart]
   ChunkRec* recs;                    // [grid]
+  ChunkOdd* odd;                     // [grid]
 };
 cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t st);
 int chunk_block_tokens();

@@ -161,3 +161,75 @@ def test_one_query_dim_far_above_the_others(cuda_dev, sa, out, decode, power):
     upload(c)
     c.check(c.run(decode=decode, scale=scale), scale=scale)
     c.check(c.run(30, 3, decode=decode, scale=scale), 30, 3, scale=scale)
+
+
+def sees(p, t, window, sinks):
+    return t <= p and (window == 0 or t > p - window or t < sinks)
+
+
+# sequences, new rows of each, window, first tokens: pairs cut between blocks
+# of threads and whole ones, pairs with rows for one tile only, several pairs
+# one after another in a block of threads
+ODD = [([300], [40], 0, 0), ([300, 77], [40, 77], 60, 4), ([9000], [20], 0, 0), ([9000, 300], [70, 1], 500, 17),
+       ([700] * 20, [300] * 20, 0, 0), ([700] * 20, [300] * 20, 150, 5), ([257] * 60, [1, 33, 64] * 20, 0, 0)]
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,rows,window,sinks", ODD)
+@pytest.mark.parametrize("value", ["nan", "-inf"])
+def test_a_value_that_is_no_number_reaches_the_rows_that_see_it_only(cuda_dev, sa, out, lens, rows, window, sinks, value):
+    """bf16 cache: rows that see a token lose the dims in which its value is no
+    number; rows that do not - before it, or with a window past it - and all
+    other dims are what they are with a zero in its place."""
+    hq, hkv = 8, 2
+    c = Case(sa, cuda_dev, lens=lens, rows=rows, hq=hq, hkv=hkv, page=16, cache="bf16", out=out, seed=205, gaps=2)
+    lost = torch.zeros((c.n_rows, hq, D), dtype=torch.bool, device=cuda_dev)
+    rng = np.random.default_rng(3)
+    marked = []
+    for b, (N, m) in enumerate(zip(lens, rows)):
+        if b % 3 == 2:
+            continue  # every third sequence stays whole
+        first = max(0, N - m - window) if window else N - m
+        for t in {N - 1, N - m, N - m // 2, max(0, N - m - 1), 2} | {int(t) for t in rng.integers(first, N, 3)}:
+            h, d = int(rng.integers(hkv)), int(rng.integers(D))
+            marked.append((int(c.table[b, t // 16]), h, t % 16, d))
+            for i in range(m):
+                if sees(N - m + i, t, window, sinks):
+                    lost[c.off[b] + i, h * 4:(h + 1) * 4, d] = True
+    for at in marked:
+        c.v[at] = 0
+    upload(c)
+    want = c.run(window, sinks)
+    for at in marked:
+        c.dv[at] = float(value)
+    got = c.run(window, sinks)
+    assert c.status() == sa.SA_OK
+    assert not torch.isfinite(got[0][lost]).any()
+    got[0][lost] = want[0][lost]
+    c.check(got, window, sinks)
+    again = c.run(window, sinks)
+    again[0][lost] = want[0][lost]
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    # one call's values leave nothing for the next
+    upload(c)
+    again = c.run(window, sinks)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,rows,window,sinks", ODD)
+def test_a_nan_key_reaches_the_rows_that_see_it_only(cuda_dev, sa, out, lens, rows, window, sinks):
+    hq, hkv = 8, 2
+    c = Case(sa, cuda_dev, lens=lens, rows=rows, hq=hq, hkv=hkv, page=16, cache="bf16", out=out, seed=206, gaps=2)
+    want = c.run(window, sinks)
+    lost = torch.zeros_like(want[1], dtype=torch.bool)
+    for b, (N, m) in enumerate(zip(lens, rows)):
+        t, h = N - 1 - m // 3, b % hkv
+        c.dk[int(c.table[b, t // 16]), h, t % 16, 77] = float("nan")
+        for i in range(m):
+            if sees(N - m + i, t, window, sinks):
+                lost[c.off[b] + i, h * 4:(h + 1) * 4] = True
+    got = c.run(window, sinks)
+    assert c.status() == sa.SA_OK
+    assert torch.isnan(got[0][lost]).all() and torch.isnan(got[1][lost]).all()
+    assert torch.equal(got[0][~lost], want[0][~lost]) and torch.equal(got[1][~lost], want[1][~lost])
