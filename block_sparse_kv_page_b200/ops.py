@@ -414,8 +414,11 @@ class PagedCache:
 
 def _on(kv: PagedCache, stream, *tensors) -> int:
     """The stream of a call on the cache's device: the given one, or that
-    device's current one.  All tensors of a call are on that device."""
+    device's current one.  All tensors of a call are on that device, which is
+    a GPU (a cache in host memory can be described and sized only)."""
     index = kv.index
+    if index < 0:
+        raise ValueError("the tensors of a call must be on a CUDA device")
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError("the tensors of a call must be on the cache's device")
@@ -470,9 +473,9 @@ def make_paged_workspace(kv: PagedCache, n_q_heads: int, stream=None) -> torch.T
     n = sparse_attn_paged_workspace_size(kv, n_q_heads)
     if n == 0:
         raise SparseAttnError(_abi.SA_ERR_INVALID, "sparse_attn_paged_workspace_size")
+    s = _on(kv, stream)
     ws = torch.empty(n, dtype=torch.uint8, device=kv.device)
-    _paged_call(kv, lib.sparse_attn_workspace_init, "sparse_attn_workspace_init", ws.data_ptr(), n,
-                _on(kv, stream))
+    _paged_call(kv, lib.sparse_attn_workspace_init, "sparse_attn_workspace_init", ws.data_ptr(), n, s)
     return ws
 
 

@@ -213,3 +213,36 @@ def test_longest_sequence(abi, lib):
         assert (lib.sparse_attn_paged_workspace_size(C.byref(kv), 32) > 0) == ok
         if not ok:
             assert set(_calls(lib, abi, kv).values()) == {abi.SA_ERR_UNSUPPORTED}
+
+
+class _Stub:
+    """A library that only notes which of its calls were reached."""
+
+    def __init__(self, real):
+        self.real, self.reached = real, []
+
+    def __getattr__(self, name):
+        if name.endswith("_size") or name.endswith("_string"):
+            return getattr(self.real, name)
+        return lambda *a: self.reached.append(name) or 0
+
+
+def test_binding_refuses_tensors_in_host_memory(monkeypatch):
+    """A forgotten .to("cuda") is an error here, not an illegal access there."""
+    import block_sparse_kv_page_b200 as sa
+    from block_sparse_kv_page_b200 import ops
+    stub = _Stub(ops.lib)
+    monkeypatch.setattr(ops, "lib", stub)
+    c = _cache()
+    off = torch.zeros(4, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    for call in (lambda: sa.sparse_attn_cache_write(c, bf(4, 2, 128), bf(4, 2, 128), off, stream=0),
+                 lambda: sa.sparse_attn_cache_write(c, bf(0, 2, 128), bf(0, 2, 128), off, ws, stream=0),
+                 lambda: sa.sparse_attn_cache_read(c, 0, bf(3, 2, 32, 128), bf(3, 2, 32, 128), stream=0),
+                 lambda: sa.sparse_attn_chunk(c, bf(4, 4, 128), off, 0.1, 0, 0, bf(4, 4, 128), None, ws, stream=0),
+                 lambda: sa.sparse_attn_paged_decode(c, bf(3, 4, 128), 0.1, 0, 0, bf(3, 4, 128), None, ws, stream=0),
+                 lambda: sa.make_paged_workspace(c, 4, stream=0)):
+        with pytest.raises(ValueError):
+            call()
+    assert not stub.reached
