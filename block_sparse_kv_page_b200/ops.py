@@ -455,6 +455,13 @@ def _row_off(row_off: torch.Tensor, kv: PagedCache) -> None:
         raise ValueError("row_off must be contiguous int32 [B + 1]")
 
 
+def _int32(x) -> int:
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:  # (ctypes keeps the low bits of others)
+        raise ValueError("first_token, window and sinks must fit 32 bits")
+    return x
+
+
 def _ws(ws: torch.Tensor | None) -> tuple[int | None, int]:
     return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
@@ -506,8 +513,9 @@ def sparse_attn_cache_read(kv: PagedCache, first_token: int, k_out: torch.Tensor
         if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous() or t.shape != k_out.shape \
                 or t.shape[0] != kv.batch or t.shape[1] != kv.n_kv_heads or t.shape[3] != 128:
             raise ValueError(f"{name} must be a contiguous bf16 [B, Hkv, cap, 128] tensor")
+    first_token = _int32(first_token)
     s = _on(kv, stream, k_out, v_out, ws)
-    _paged_call(kv, lib.sparse_attn_cache_read, "sparse_attn_cache_read", kv.ref, int(first_token),
+    _paged_call(kv, lib.sparse_attn_cache_read, "sparse_attn_cache_read", kv.ref, first_token,
                 k_out.data_ptr(), v_out.data_ptr(), k_out.shape[2], *_ws(ws), s)
 
 
@@ -530,11 +538,12 @@ def sparse_attn_chunk(kv: PagedCache, q: torch.Tensor, row_off: torch.Tensor, sc
     rows, heads, _ = q.shape
     out_dtype = _attn_out(rows, heads, out, lse)
     _row_off(row_off, kv)
+    window, sinks = _int32(window), _int32(sinks)
     s = _on(kv, stream, q, row_off, out, lse, ws)
     if rows == 0:
         return
     _paged_call(kv, lib.sparse_attn_chunk, "sparse_attn_chunk", kv.ref, q.data_ptr(), stride, heads,
-                row_off.data_ptr(), rows, int(window), int(sinks), float(scale), out.data_ptr(), out_dtype,
+                row_off.data_ptr(), rows, window, sinks, float(scale), out.data_ptr(), out_dtype,
                 _ptr(lse), *_ws(ws), s)
 
 
@@ -547,6 +556,7 @@ def sparse_attn_paged_decode(kv: PagedCache, q: torch.Tensor, scale: float, wind
     if rows != kv.batch:
         raise ValueError("q must have one row per sequence")
     out_dtype = _attn_out(rows, heads, out, lse)
+    window, sinks = _int32(window), _int32(sinks)
     s = _on(kv, stream, q, out, lse, ws)
     _paged_call(kv, lib.sparse_attn_paged_decode, "sparse_attn_paged_decode", kv.ref, q.data_ptr(), stride,
-                heads, int(window), int(sinks), float(scale), out.data_ptr(), out_dtype, _ptr(lse), *_ws(ws), s)
+                heads, window, sinks, float(scale), out.data_ptr(), out_dtype, _ptr(lse), *_ws(ws), s)

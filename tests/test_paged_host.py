@@ -246,3 +246,19 @@ def test_binding_refuses_tensors_in_host_memory(monkeypatch):
         with pytest.raises(ValueError):
             call()
     assert not stub.reached
+
+
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 16, -(1 << 31) - 1, 10 ** 12])
+def test_binding_refuses_numbers_past_32_bits(value):
+    """ctypes would keep their low 32 bits: a window of 2^32 + 16 would be 16."""
+    import block_sparse_kv_page_b200 as sa
+    c = _cache()
+    off = torch.zeros(4, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    for call in (lambda: sa.sparse_attn_cache_read(c, value, bf(3, 2, 32, 128), bf(3, 2, 32, 128)),
+                 lambda: sa.sparse_attn_chunk(c, bf(4, 4, 128), off, 0.1, value, 0, bf(4, 4, 128), None, None),
+                 lambda: sa.sparse_attn_chunk(c, bf(4, 4, 128), off, 0.1, 5, value, bf(4, 4, 128), None, None),
+                 lambda: sa.sparse_attn_paged_decode(c, bf(3, 4, 128), 0.1, value, 0, bf(3, 4, 128), None, None),
+                 lambda: sa.sparse_attn_paged_decode(c, bf(3, 4, 128), 0.1, 5, value, bf(3, 4, 128), None, None)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
