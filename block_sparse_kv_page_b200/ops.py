@@ -98,9 +98,20 @@ def sparse_attn_workspace_size(kv: KvCache, n_q_heads: int, n_q_rows: int, max_s
     return int(lib.sparse_attn_workspace_size(C.byref(kv.desc), n_q_heads, n_q_rows, max_sel))
 
 
+def _ws_call(ws: torch.Tensor, stream, fn, where: str, *args) -> None:
+    """A call on a workspace alone, with its device current: on the given
+    stream or that device's current one."""
+    index = ws.get_device()
+    if index < 0 or index == torch._C._cuda_getDevice():
+        _check(fn(ws.data_ptr(), *args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(index):
+            _check(fn(ws.data_ptr(), *args, _stream(stream)), where)
+
+
 def sparse_attn_workspace_init(ws: torch.Tensor, stream=None) -> None:
-    _check(lib.sparse_attn_workspace_init(ws.data_ptr(), ws.numel() * ws.element_size(),
-                                          _stream(stream)), "sparse_attn_workspace_init")
+    _ws_call(ws, stream, lib.sparse_attn_workspace_init, "sparse_attn_workspace_init",
+             ws.numel() * ws.element_size())
 
 
 def make_workspace(kv: KvCache, n_q_heads: int, n_q_rows: int, max_sel: int, stream=None) -> torch.Tensor:
@@ -345,8 +356,7 @@ def sparse_attn_route(kv: KvCache, meta: torch.Tensor, rule, q: torch.Tensor, n_
 
 def sparse_attn_get_device_status(ws: torch.Tensor, stream=None) -> int:
     out = C.c_int(0)
-    _check(lib.sparse_attn_get_device_status(ws.data_ptr(), C.byref(out), _stream(stream)),
-           "sparse_attn_get_device_status")
+    _ws_call(ws, stream, lib.sparse_attn_get_device_status, "sparse_attn_get_device_status", C.byref(out))
     return int(out.value)
 
 

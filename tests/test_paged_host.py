@@ -262,3 +262,52 @@ def test_binding_refuses_numbers_past_32_bits(value):
                  lambda: sa.sparse_attn_paged_decode(c, bf(3, 4, 128), 0.1, 5, value, bf(3, 4, 128), None, None)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_workspace_calls_run_on_the_workspace_s_device(monkeypatch):
+    """Status and initialisation of a workspace on a device that is not the
+    current one: on that device's current stream, behind its calls."""
+    import block_sparse_kv_page_b200 as sa
+    from block_sparse_kv_page_b200 import ops
+    seen, now = [], [0]
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, now[0], a[-1])) or 0
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.index
+
+        def __exit__(self, *e):
+            now[0] = self.was
+
+    class Workspace:
+        def __init__(self, index):
+            self.index = index
+
+        def get_device(self):
+            return self.index
+
+        def data_ptr(self):
+            return 0x100
+
+        def numel(self):
+            return 512
+
+        def element_size(self):
+            return 1
+
+    monkeypatch.setattr(ops, "lib", Lib())
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("S", (), {"cuda_stream": 700 + now[0]}))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 700 + i, raising=False)
+    for index in (0, 1):
+        sa.sparse_attn_workspace_init(Workspace(index))
+        assert sa.sparse_attn_get_device_status(Workspace(index)) == 0
+        assert sa.sparse_attn_get_device_status(Workspace(index), 5) == 0
+    assert [(d, s) for _, d, s in seen] == [(0, 700), (0, 700), (0, 5), (1, 701), (1, 701), (1, 5)]
