@@ -12,6 +12,9 @@ w of every weight moves it by at most w * sum p_t |v_t|:
 and the output is rounded once: 2^-8 of it (bf16) or 2^-24 (fp32).
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -23,6 +26,7 @@ from test_gpu_paged import Case
 pytestmark = pytest.mark.gpu
 
 D = 128
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -233,3 +237,55 @@ def test_a_nan_key_reaches_the_rows_that_see_it_only(cuda_dev, sa, out, lens, ro
     assert c.status() == sa.SA_OK
     assert torch.isnan(got[0][lost]).all() and torch.isnan(got[1][lost]).all()
     assert torch.equal(got[0][~lost], want[0][~lost]) and torch.equal(got[1][~lost], want[1][~lost])
+
+
+def test_first_calls_from_several_threads(cuda_dev):
+    """In a process of its own: the first launches of kernels that ask for
+    different amounts of shared memory, from threads at once."""
+    code = """
+import threading, torch
+import block_sparse_kv_page_b200 as sa
+dev, D = torch.device("cuda:0"), 128
+made = []
+for i in range(12):
+    g = torch.Generator().manual_seed(i % 3)
+    dt = torch.float8_e4m3fn if i & 1 else torch.bfloat16
+    k, v = (torch.randn(40, 2, 16, D, generator=g).to(dt).to(dev) for _ in range(2))
+    sc = torch.full((40, 2, 16), 127, dtype=torch.uint8, device=dev) if i & 1 else None
+    table = torch.randperm(40, generator=g).to(torch.int32)[None].to(dev)
+    kv = sa.PagedCache(k, v, table, torch.tensor([600], dtype=torch.int32, device=dev), k_scale=sc, v_scale=sc)
+    decode = i % 3 == 0
+    rows = 1 if decode else 50
+    q = torch.randn(rows, 8, D, generator=g).to(torch.bfloat16).to(dev)
+    out = torch.zeros(rows, 8, D, device=dev, dtype=torch.float32 if i & 2 else torch.bfloat16)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=dev)
+    made.append((kv, decode, q, out, off, sa.make_paged_workspace(kv, 8), torch.cuda.Stream()))
+def call(m, out):
+    kv, decode, q, _, off, ws, s = m
+    if decode:
+        sa.sparse_attn_paged_decode(kv, q, 0.1, 0, 0, out, None, ws, s)
+    else:
+        sa.sparse_attn_chunk(kv, q, off, 0.1, 0, 0, out, None, ws, s)
+torch.cuda.synchronize()
+start, failed = threading.Barrier(len(made)), []
+def work(m):
+    start.wait()
+    try:
+        for _ in range(5):
+            call(m, m[3])
+    except Exception as e:
+        failed.append(e)
+threads = [threading.Thread(target=work, args=(m,)) for m in made]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not failed, failed
+for m in made:
+    again = torch.zeros_like(m[3])
+    call(m, again)
+    torch.cuda.synchronize()
+    assert torch.equal(again, m[3])
+    assert sa.sparse_attn_get_device_status(m[5]) == sa.SA_OK
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=150)
+    assert run.returncode == 0, run.stderr[-2000:]
