@@ -218,42 +218,55 @@ bool encode_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, 
 }
 
 cudaError_t set_smem_attr(const void* func, size_t bytes) {
+  constexpr int kDevices = 64;
   struct Entry {
-    const void* f;
-    int dev;
-    size_t bytes;
+    std::atomic<const void*> func{nullptr};
+    std::atomic<size_t> bytes[kDevices]{};  // allowed so far
   };
-  static Entry cache[64];
-  static int n = 0;
+  static Entry table[64];
+  static std::atomic_flag busy = ATOMIC_FLAG_INIT;  // one thread at a time raises a limit
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
-  for (int i = 0; i < n; ++i)
-    if (cache[i].f == func && cache[i].dev == dev && cache[i].bytes >= bytes) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e != cudaSuccess) return e;
-  for (int i = 0; i < n; ++i)
-    if (cache[i].f == func && cache[i].dev == dev) {
-      cache[i].bytes = bytes;
-      return cudaSuccess;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  std::atomic<size_t>* allowed = nullptr;
+  for (Entry& t : table) {
+    const void* f = t.func.load(std::memory_order_acquire);
+    if (f == nullptr && t.func.compare_exchange_strong(f, func)) f = func;
+    if (f == func) {
+      if (dev >= 0 && dev < kDevices) allowed = &t.bytes[dev];
+      break;
     }
-  if (n < 64) cache[n++] = Entry{func, dev, bytes};
-  return cudaSuccess;
+  }
+  if (allowed && allowed->load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  while (busy.test_and_set(std::memory_order_acquire)) {
+  }
+  cudaError_t r = cudaSuccess;
+  if (!allowed || allowed->load(std::memory_order_relaxed) < bytes) {
+    r = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (r == cudaSuccess && allowed) allowed->store(bytes, std::memory_order_release);
+  }
+  busy.clear(std::memory_order_release);
+  return r;
 }
 
 int device_sm_count() {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return 148;
   }
-  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
-  int n = 0;
+  const bool kept = dev >= 0 && dev < 64;
+  int n = kept ? cache[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     return 148;
   }
-  if (dev >= 0 && dev < 64) cache[dev] = n;
+  if (kept) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

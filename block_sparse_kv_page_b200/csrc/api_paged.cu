@@ -4,7 +4,6 @@
 // Workspace: the layout of the other calls (api.cu): the status word at 0, the
 // unit counters (not used here, left as they are), per-call scratch from
 // kScratch on.
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <numeric>
@@ -14,31 +13,6 @@
 #include "paged.h"
 
 namespace sa {
-
-cudaError_t allow_smem(const void* func, size_t bytes) {
-  struct Entry {
-    std::atomic<const void*> func{nullptr};
-    std::atomic<uint64_t> devices{0};  // bit d: set on device d
-  };
-  static Entry table[16];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  Entry* mine = nullptr;
-  for (Entry& t : table) {
-    const void* f = t.func.load(std::memory_order_acquire);
-    if (f == nullptr && t.func.compare_exchange_strong(f, func)) f = func;
-    if (f == func) {
-      mine = &t;
-      break;
-    }
-  }
-  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-  if (mine && (mine->devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && mine) mine->devices.fetch_or(bit, std::memory_order_release);
-  return e;
-}
 
 namespace {
 

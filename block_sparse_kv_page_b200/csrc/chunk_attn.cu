@@ -1333,7 +1333,7 @@ cudaError_t launch(const ChunkArgs& a, int grid, cudaStream_t st) {
   auto* k = chunk_kernel<E4M3, TERMS>;
   constexpr int smem = Shape<TERMS>::smem(E4M3);
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-  const cudaError_t e = allow_smem((const void*)k, smem);
+  const cudaError_t e = set_smem_attr((const void*)k, smem);
   if (e != cudaSuccess) return e;
   // The split waits for ever if it asks for more than the block was given.
   static const bool fits = [&] {

@@ -50,7 +50,8 @@ bool encode_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, 
                     const unsigned long long* dims, const unsigned long long* strides, const unsigned* box,
                     bool swizzle, bool wide);
 // Opt a kernel into `bytes` of dynamic shared memory on the current device
-// (cached per device and kernel, so repeated launches skip the driver call).
+// (remembered per device and kernel, so repeated launches skip the driver call;
+// any thread may call it).
 cudaError_t set_smem_attr(const void* func, size_t bytes);
 
 // Launch with programmatic stream serialisation (programmatic dependent

@@ -103,8 +103,5 @@ int paged_decode_grid(int sms);
 size_t paged_decode_part_floats();   // per CTA
 // recs: entries of a.recs, the smaller of units and grid
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int grid, int recs, cudaStream_t st);
-// Opt a kernel into `bytes` of dynamic shared memory on the current device
-// (remembered per device; any thread may call it).
-cudaError_t allow_smem(const void* func, size_t bytes);
 
 }  // namespace sa

@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const __grid_consta
 template <bool E4M3, int TERMS>
 cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   auto* k = paged_decode_kernel<E4M3, TERMS>;
-  const cudaError_t e = allow_smem((const void*)k, Ring<E4M3>::kSmem);
+  const cudaError_t e = set_smem_attr((const void*)k, Ring<E4M3>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, (unsigned)grid, kThreads, Ring<E4M3>::kSmem, st, a);
 }
