@@ -7,6 +7,7 @@
 // tokens, 8 heads, written in 170 us (5.6 TB/s), read back in 183 us (5.5); a
 // copy reaches 6.5.
 #include "paged.cuh"
+#include "internal.h"
 
 namespace sa {
 namespace {
@@ -193,7 +194,8 @@ cudaError_t launch_cache_read(CacheReadArgs a, cudaStream_t st) {
   a.items = (unsigned)items;
   const long long per = kReadThreads / 32;
   long long blocks = (2 * items + per - 1) / per;
-  if (blocks > 148 * 16) blocks = 148 * 16;
+  const long long most = 16LL * device_sm_count();
+  if (blocks > most) blocks = most;
   if (a.kv.e4m3) cache_read_kernel<true><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, (unsigned)tiles);
   else cache_read_kernel<false><<<(unsigned)blocks, kReadThreads, 0, st>>>(a, (unsigned)tiles);
   return cudaGetLastError();

@@ -19,12 +19,8 @@ SA_DEV int paged_tokens(const PagedView& kv, int b, int* status) {
 }
 
 // New rows [r0, r0 + return value) of sequence b; none (flagged) for a range
-// outside the row arrays.  row_off null: row b.
+// outside the row arrays.
 SA_DEV int paged_rows(const int32_t* row_off, int n_rows, int b, int& r0, int* status) {
-  if (row_off == nullptr) {
-    r0 = b;
-    return 1;
-  }
   r0 = __ldg(row_off + b);
   const int r1 = __ldg(row_off + b + 1);
   if (r0 < 0 || r1 < r0 || r1 > n_rows) {

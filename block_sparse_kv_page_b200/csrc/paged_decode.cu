@@ -14,8 +14,8 @@
 // kC0 tiles more, the cost of starting one), cut anywhere, so that one long
 // sequence fills every SM and ragged batches stay balanced.  The prefix is
 // computed from the lengths on the device by every CTA.  A unit cut between
-// CTAs leaves unnormalised parts in the workspace, merged by combine_kernel in
-// CTA order: results do not depend on scheduling.
+// CTAs leaves unnormalised parts in the workspace, merged by
+// decode_combine_kernel in CTA order: results do not depend on scheduling.
 //
 // Inside a CTA the four warps take tiles in turn, each with a ring of its own:
 // TMA boxes of 16 rows, 128B-swizzled, three CTAs and 192 KiB of rings per SM.
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_
   }
   __syncthreads();
   grid_dep_wait();
-  grid_dep_trigger();  // combine_kernel may be scheduled; it waits for this grid's end
+  grid_dep_trigger();  // decode_combine_kernel may be scheduled; it waits for this grid's end
 
   // ---- this CTA's run of the work
   auto prefix = [&](long long v, long long& total) -> long long {
