@@ -335,3 +335,28 @@ def test_every_value_row_counts_once(cuda_dev, sa, out, cache, page, decode):
             got = c.run(window, sinks, decode=decode)
             check_rows(c, got, 1 / math.sqrt(D), None, decode, window, sinks)
     assert c.status() == sa.SA_OK
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("scale_byte", [0, 255])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3)])
+def test_scale_bytes_of_hidden_tokens_may_be_anything(cuda_dev, sa, out, decode, scale_byte, window, sinks):
+    """Slots past a sequence's end, spare pages and tokens that a window has
+    passed: bit for bit as with ordinary scale bytes there."""
+    lens = [517, 33, 256, 70]
+    rows = [1] * 4 if decode else [40, 33, 1, 65]
+    c = Case(sa, cuda_dev, lens=lens, rows=rows, hq=8, hkv=2, page=64, cache="e4m3", out=out, seed=208, stale=0x7f)
+    want = c.run(window, sinks, decode=decode)
+    c.check(want, window, sinks)
+    live = torch.zeros(c.ks.shape[0], 64, dtype=torch.bool)
+    for b, (N, m) in enumerate(zip(lens, rows)):
+        for t in range(N):
+            if window == 0 or t >= max(0, N - m - window + 1) or t < sinks:
+                live[int(c.table[b, t // 64]), t % 64] = True
+    for held in (c.ks, c.vs):
+        held[~live[:, None, :].expand(-1, 2, -1)] = scale_byte
+    upload(c)
+    got = c.run(window, sinks, decode=decode)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert c.status() == sa.SA_OK
