@@ -5,9 +5,9 @@
 // of KV head g: z_t = scale q . k_t over the visible tokens t (t <= p, inside
 // the window or among the first tokens), out = sum exp(z_t - lse) v_t, by one
 // pass over the tokens with a running reference maximum and sum.  Measured: 2048
-// rows over 32k tokens, 28 heads, bf16: 1.07 ms under the power cap (870
-// TFLOP/s; 950 in short runs); four prompts of up to 2048 tokens, 32 heads:
-// 175 us, from e4m3 235.
+// rows over 32k tokens, 28 heads, bf16: 1.07 ms (870 TFLOP/s; the tensor pipe is
+// 45% busy: QK, softmax and PV wait for one another, and for shared memory); four
+// prompts of up to 2048 tokens, 32 heads, e4m3: 234 us.
 //
 // Units.  A query vector is a (row, query head) pair.  The G heads of a KV head
 // and R = floor(128 / G) consecutive rows make a tile of up to 128 vectors (M of
@@ -65,11 +65,11 @@
 // tile; so a look at the first vector's result shows it.  combine_kernel then
 // looks through those V rows, and takes the dims that have such a value again,
 // token by token.  (A bf16 cache only: what the converters write are numbers.
-// Four bf16 prompts 127 -> 129.5 us, 16 rows over 29.5k tokens 43.8 -> 46.4;
+// Four bf16 prompts 127 -> 130 us, 16 rows over 29.5k tokens 43.8 -> 46.9;
 // looking through the V rows ahead of PV cost the prompts 1 to 38 us and the
 // short calls 2 to 6, by whichever warps.)
 //
-// P is rounded to bf16 where the output is bf16 (its error, 2^-9 per weight, is
+// P is rounded to bf16 where the output is bf16 (its error, 2^-8 per weight, is
 // that of the output's own rounding); for fp32 outputs it is split into three
 // bf16 terms (24 bits), which leaves room for one S buffer per slot.
 #include "paged.cuh"

@@ -4,7 +4,7 @@
 // head g: out = sum exp(z_t - lse) v_t over the visible tokens, z_t = scale
 // q . k_t, in one pass with a running maximum and sum.  Every visible token's K
 // and V are read once for the G <= 8 heads that share them; that read bounds it.
-// Measured: 32 sequences of up to 32k tokens, 8 KV heads, e4m3: 224 us, 5.1
+// Measured: 32 sequences of up to 32k tokens, 8 KV heads, e4m3: 228 us, 5.0
 // TB/s; one of 29.5k tokens, 4 KV heads, bf16: 21 us, where the read itself
 // takes 9.4 and the rest is latency (lengths, table, first tiles, merge).
 //
@@ -22,7 +22,7 @@
 // Per tile (tensor cores, fp32 accumulation):
 //   S^T [16 tokens x 8 heads] = K Q^T;
 //   P: exp2 of the scaled scores in fp32, as two bf16 terms (three for fp32
-//      outputs: 2^-17 and 2^-25 of a weight), moved to the B layout;
+//      outputs: 2^-16 and 2^-24 of a weight), moved to the B layout;
 //   O^T [128 dims x 8 heads] += V^T P^T.
 // e4m3: codes become fragments in registers.  The order of the reduction
 // axis is free as long as both operands share it, so a lane takes whole 16-byte
@@ -32,7 +32,7 @@
 // relative to the largest scale seen, which is followed like the maximum; tiles
 // with a weight below what f16 holds take the same products in bf16 (whose
 // conversion, by shifts and masks, costs three times as much: 16 sequences of
-// 32k tokens 188 us, 224 where every tile takes it).  The rows' scales (powers of two)
+// 32k tokens 187 us, 223 where every tile takes it).  The rows' scales (powers of two)
 // multiply the scores and the weights, 4 values a lane instead of 256.
 #include <cuda_fp16.h>
 

@@ -469,7 +469,9 @@ sa_status sparse_attn_cache_write(const sa_paged_desc* kv, const void* k_new, co
  * [cap_tokens][128], the contiguous cache of sa_kv_desc; row t holds token t.
  * first_token as in sparse_attn_build_meta (>= 0: t0_b = first_token; < 0:
  * t0_b = max(0, N_b + first_token)).  Rows outside the range are not written;
- * tokens at and past cap_tokens are not read back (SA_ERR_DEVICE_CHECK). */
+ * tokens at and past cap_tokens are not read back (SA_ERR_DEVICE_CHECK).
+ * SA_ERR_UNSUPPORTED where B * n_kv_heads * max_pages * page_size / 16 reaches
+ * 2^30. */
 sa_status sparse_attn_cache_read(const sa_paged_desc* kv, int32_t first_token, void* k_out,
                                  void* v_out, int64_t cap_tokens, void* ws, size_t ws_bytes,
                                  void* stream);
@@ -481,24 +483,32 @@ sa_status sparse_attn_cache_read(const sa_paged_desc* kv, int32_t first_token, v
  *   t < sinks (the first tokens, which stay visible).
  * q: bf16, value d of (row, query head) at row * q_row_stride + head * 128 +
  * d (q_row_stride a multiple of 8, >= n_q_heads * 128), 16-byte aligned.
- * z = scale * q . k, softmax in fp32; out [n_rows][n_q_heads][128], fp32 or
- * bf16 (16-byte aligned); lse (nullable) fp32 [n_rows][n_q_heads], the natural
- * logarithm of the sum of exp(z).  A row that sees nothing gets out = 0 and
- * lse = -inf.  What is held past N_b, or where no row of the sequence looks,
- * may be anything, NaN included; a NaN in q, or in a bf16 key that a row sees,
- * makes that row NaN; a NaN or infinity in a bf16 value that a row sees makes
- * its dim of the row NaN or infinite.  Rows that do not see it are not touched
- * (the dims around such a value are then computed again one by one, which is
- * slow).  A NaN code of an e4m3 row that is seen, and infinities in q or keys,
- * give undefined results.  Any m_b from 0 on; lengths are read on the
- * device only, so a captured call replays with other lengths.  Two launches. */
+ * z = scale * q . k with fp32 sums, weights and their sum in fp32; for the
+ * product with V each weight is represented in fewer bits, relative to itself:
+ * three bf16 terms for fp32 outputs (2^-24), one bf16 term (2^-8) for bf16
+ * outputs.  What lies below 2^-106 of a row's largest weight may count as
+ * zero. out [n_rows][n_q_heads][128], fp32 or bf16 (16-byte aligned); lse
+ * (nullable) fp32 [n_rows][n_q_heads], the natural logarithm of the sum of
+ * exp(z).  A row that sees nothing gets out = 0 and lse = -inf.  What is held
+ * past N_b, or where no row of the sequence looks, may be anything, NaN
+ * included; a NaN in q, or in a bf16 key that a row sees, makes that row NaN;
+ * a NaN or infinity in a bf16 value that a row sees makes its dim of the row
+ * NaN or infinite.  Rows that do not see it are not touched (the dims around
+ * such a value are then computed again one by one, which is slow).  A NaN code
+ * of an e4m3 row that is seen, and infinities in q or keys, give undefined
+ * results.  Any m_b from 0 on; lengths are read on the device only, so a
+ * captured call replays with other lengths.  Two launches. */
 sa_status sparse_attn_chunk(const sa_paged_desc* kv, const void* q, int64_t q_row_stride,
                             int32_t n_q_heads, const int32_t* row_off, int32_t n_rows,
                             int32_t window, int32_t sinks, float scale, void* out,
                             int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* (g4) The single-token form: one row per sequence (row b at position
- * N_b - 1), otherwise as sparse_attn_chunk. */
+ * N_b - 1), otherwise as sparse_attn_chunk.  Weights for the product with V:
+ * three (fp32 outputs) or two (bf16 outputs) bf16 terms, 2^-24 or 2^-16 of a
+ * weight; from e4m3 also two or one f16 terms, 2^-19 or 2^-11, in tiles whose
+ * weights times V scales f16 holds that well.  What lies below 2^-126 of the
+ * largest weight, or of the largest weight times V scale, may count as zero. */
 sa_status sparse_attn_paged_decode(const sa_paged_desc* kv, const void* q, int64_t q_row_stride,
                                    int32_t n_q_heads, int32_t window, int32_t sinks, float scale,
                                    void* out, int32_t out_dtype, float* lse, void* ws,
