@@ -60,6 +60,8 @@ def check_rows(c, got, scale, zmax, decode, window=0, sinks=0):
     bf = c.out_dtype == torch.bfloat16
     G = c.hq // c.hkv
     for b, (N, m) in enumerate(zip(c.lens, c.rows)):
+        if not m:
+            continue
         r0 = c.off[b]
         for h in range(c.hkv):
             k, v, ok = c.held(b, h)
