@@ -362,3 +362,41 @@ def test_scale_bytes_of_hidden_tokens_may_be_anything(cuda_dev, sa, out, decode,
     got = c.run(window, sinks, decode=decode)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert c.status() == sa.SA_OK
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("longest", [40, 9000])
+def test_nan_queries_with_bf16_outputs(cuda_dev, sa, cache, decode, longest):
+    """Also the first vector of a tile, which is looked at for values that are no numbers."""
+    lens = [longest, 33, longest // 2]
+    rows = [1] * 3 if decode else [20, 3, 7]
+    c = Case(sa, cuda_dev, lens=lens, rows=rows, hq=8, hkv=2, page=16, cache=cache, out="bf16", seed=209)
+    want = c.run(decode=decode)
+    c.check(want)
+    lost = ((0, 0), (1, 3), (2, 7))
+    for r, h in lost:
+        c.dq[r, h, 5] = float("nan")
+    out, lse = c.run(decode=decode)
+    for r, h in lost:
+        assert torch.isnan(out[r, h]).all() and torch.isnan(lse[r, h])
+        out[r, h], lse[r, h] = want[0][r, h], want[1][r, h]
+    # (not bit for bit: the rows of two warps raise their references together, so
+    # one row's scores may choose the one that another's weights are rounded against)
+    c.check((out, lse))
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5)])
+def test_a_nan_value_in_the_single_token_form(cuda_dev, sa, out, window, sinks):
+    """Its dim of the heads that share it, if the window or the first tokens
+    show it; nothing where they do not."""
+    c = Case(sa, cuda_dev, lens=[5000, 70], rows=[1, 1], hq=8, hkv=2, page=16, cache="bf16", out=out, seed=210)
+    want = c.run(window, sinks, decode=True)
+    for t, d in ((1234, 9), (4990, 100), (3, 50)):
+        c.dv[int(c.table[0, t // 16]), 1, t % 16, d] = float("nan")
+    got = c.run(window, sinks, decode=True)
+    lost = torch.zeros_like(got[0], dtype=torch.bool)
+    lost[0, 4:, [100, 50] + ([] if window else [9])] = True
+    assert torch.isnan(got[0][lost]).all()
+    assert torch.equal(got[0][~lost], want[0][~lost]) and torch.equal(got[1], want[1])
