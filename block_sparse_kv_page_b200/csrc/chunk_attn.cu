@@ -81,8 +81,8 @@ namespace {
 
 constexpr int kC0 = 2;              // cost of starting a pair, in blocks
 // Least work of a CTA: small calls are a chain of latencies and so spread widely
-// (16 rows over 2k tokens, 4 KV heads, in a graph: 20.6 us; shares of 4 and 6:
-// 21.4 and 25.7).
+// (16 rows over 2k tokens, 4 KV heads, bf16, fp32 outputs, in a graph: 22.4 us;
+// shares of 4 and 6: 23.2 and 27.6).
 constexpr int kMinShare = kC0 + 1;
 constexpr int kInfo = 16;
 constexpr int BLK = 64;             // tokens of a block

@@ -49,7 +49,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kC0 = 6;          // cost of starting a unit, in tiles
 // Least work of a CTA: small calls are a chain of latencies, so they are spread
 // as far as a start's cost allows (1 sequence of 2k tokens, 4 KV heads, in a
-// graph: 7.5 us; shares of 10, 14, 18 and 24: 9.0, 9.9, 11.1, 12.3).
+// graph: 7.7 us; shares of 10, 14, 18 and 24: 9.0, 9.9, 11.1, 12.3).
 constexpr int kMinShare = kC0;
 constexpr int kPart = kHeadDim + 4;          // floats of a head's part: acc, maximum, sum, 2 unused
 constexpr int kMergeBytes = kWarps * kMaxGroup * (kHeadDim + 2) * 4;
