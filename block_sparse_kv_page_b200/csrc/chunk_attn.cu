@@ -1119,84 +1119,162 @@ __global__ void __launch_bounds__(Regs<E4M3>::kThreads, 1) chunk_kernel(const __
 // What follows is for a bf16 cache with values that are no numbers in V rows that
 // some rows of a pair see and others do not.
 
-// Whether there are such values, in the dims that this lane has (a warp, 4 dims a lane).
-SA_DEV bool odd_values(const ChunkArgs& a, int b, int g, const Geom& q) {
+// Dims of this lane (a bit each; a warp, 4 dims a lane) in which the row at position
+// p has lost its result to a value that it does not see, and would not have lost
+// it to one that it sees.
+SA_DEV uint32_t dims_to_take(const ChunkArgs& a, int b, int g, const Geom& q, int p) {
   const PagedView& kv = a.p.kv;
-  const int before = a.p.window ? max(q.p1 - a.p.window + 1 - q.lo, 0) : 0, all = before + q.rows - 1;
-  bool odd = false;
+  const int window = a.p.window, sinks = a.p.sinks;
+  // (and the first row's own token, which all see: with it a whole call of NaN needs nothing)
+  const int before = window ? max(q.p1 - window + 1 - q.lo, 0) : 0, all = before + q.rows;
+  uint32_t seen = 0u, others = 0u;
+#pragma unroll 4
   for (int x = 0; x < all; ++x) {
-    const int t = x < before ? q.lo + x : q.p0 + 1 + x - before;
+    const int t = x < before ? q.lo + x : q.p0 + x - before;
     if (t < 0) continue;
     const int e = t / kv.page_size, page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
     if (page < 0 || page >= kv.n_pages) continue;
     const uint2 w = __ldg(reinterpret_cast<const uint2*>(kv.v + paged_offset(kv, page, g, t - e * kv.page_size)) +
                           (threadIdx.x & 31));
-    const uint32_t x0 = (w.x & 0x7f807f80u) + 0x00800080u, x1 = (w.y & 0x7f807f80u) + 0x00800080u;
-    odd |= ((x0 | x1) & 0x80008000u) != 0u;  // a half with an exponent of 255
+    // the top bits of halves with an exponent of 255
+    const uint32_t x0 = ((w.x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    const uint32_t x1 = ((w.y & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    const uint32_t dims = ((x0 >> 15) & 1u) | ((x0 >> 30) & 2u) | ((x1 >> 13) & 4u) | ((x1 >> 28) & 8u);
+    if (t <= p && (!window || t > p - window || t < sinks)) seen |= dims;
+    else others |= dims;
   }
-  return odd;
+  return others & ~seen;
 }
 
-// Row `row` of sequence b at position p, query head h, token by token: a warp, 4 dims a lane.
+// One more token of a softmax: score z (log2 units; -inf: not seen), D dims of its value.
+template <int D>
+SA_DEV void next_token(float z, const uint32_t (&v)[D / 2], float& m, float& l, float (&o)[D]) {
+  const float ninf = -__int_as_float(0x7f800000);
+  const float mn = fmaxf(m, z), f = mn == ninf ? 1.f : fast_exp2(m - mn);
+  const float w = z == ninf ? 0.f : fast_exp2(z - mn);
+  m = mn;
+  l = l * f + w;
+#pragma unroll
+  for (int d = 0; d < D; d += 2) {
+    o[d] = o[d] * f + (z == ninf ? 0.f : w * bf16_lo(v[d / 2]));
+    o[d + 1] = o[d + 1] * f + (z == ninf ? 0.f : w * bf16_hi(v[d / 2]));
+  }
+}
+
+// Row `row` of sequence b at position p, query head h: a warp, 4 dims a lane.
 SA_DEV float4 again_vector(const ChunkArgs& a, int b, int row, int p, int h) {
   const PagedView& kv = a.p.kv;
   const int lane = threadIdx.x & 31, g = h / a.p.G;
   const float ninf = -__int_as_float(0x7f800000);
   const uint2 qw = *reinterpret_cast<const uint2*>(a.p.q + (size_t)row * a.p.q_row_stride + (size_t)h * kHeadDim + 4 * lane);
-  const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
   const int lo = a.p.window && p >= a.p.window ? p - a.p.window + 1 : 0, first = min(a.p.window ? a.p.sinks : 0, lo);
-  float m = ninf, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = 0; x < first + p + 1 - lo; ++x) {
-    const int t = x < first ? x : lo + x - first, e = t / kv.page_size;
-    const int page = __ldg(kv.table + (size_t)b * kv.max_pages + e);
-    if (page < 0 || page >= kv.n_pages) continue;
-    const long long at = paged_offset(kv, page, g, t - e * kv.page_size) + 8 * lane;
-    const uint2 k = __ldg(reinterpret_cast<const uint2*>(kv.k + at)), v = __ldg(reinterpret_cast<const uint2*>(kv.v + at));
-    float z = q[0] * bf16_lo(k.x) + q[1] * bf16_hi(k.x) + q[2] * bf16_lo(k.y) + q[3] * bf16_hi(k.y);
+  const int all = first + p + 1 - lo;
+  float m = ninf, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int x0 = 0; x0 < all; x0 += 32) {  // 32 tokens: a lane looks up the place of one, then 4 at a time
+    const int t = x0 + lane < first ? x0 + lane : lo + x0 + lane - first, e = t / kv.page_size;
+    const int page = x0 + lane < all ? __ldg(kv.table + (size_t)b * kv.max_pages + e) : -1;
+    const int slot = t - e * kv.page_size;
+#pragma unroll 1
+    for (int y = 0; y < min(32, all - x0); y += 4) {
+      uint2 k[4], v[4];
+      bool in[4];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-    z *= a.scale_log2;
-    const float mn = fmaxf(m, z), f = mn == ninf ? 1.f : fast_exp2(m - mn);
-    const float w = z == ninf ? 0.f : fast_exp2(z - mn);
-    m = mn;
-    l = l * f + w;
-    o.x = o.x * f + w * bf16_lo(v.x);
-    o.y = o.y * f + w * bf16_hi(v.x);
-    o.z = o.z * f + w * bf16_lo(v.y);
-    o.w = o.w * f + w * bf16_hi(v.y);
+      for (int u = 0; u < 4; ++u) {
+        const int pg = __shfl_sync(0xffffffffu, page, y + u), sl = __shfl_sync(0xffffffffu, slot, y + u);
+        in[u] = pg >= 0 && pg < kv.n_pages;
+        const long long at = paged_offset(kv, in[u] ? pg : 0, g, in[u] ? sl : 0) + 8 * lane;
+        k[u] = __ldg(reinterpret_cast<const uint2*>(kv.k + at));
+        v[u] = __ldg(reinterpret_cast<const uint2*>(kv.v + at));
+      }
+      float z[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        z[u] = bf16_lo(qw.x) * bf16_lo(k[u].x) + bf16_hi(qw.x) * bf16_hi(k[u].x) + bf16_lo(qw.y) * bf16_lo(k[u].y) +
+               bf16_hi(qw.y) * bf16_hi(k[u].y);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) z[u] += __shfl_xor_sync(0xffffffffu, z[u], s);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t vu[2] = {v[u].x, v[u].y};
+        next_token<4>(in[u] ? z[u] * a.scale_log2 : ninf, vu, m, l, o);
+      }
+    }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  return make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
 }
 
-// The 8 dims from 4 d4 of a lane's vector - row `row` of a cut pair, query head h -
-// where the merge of its parts gave some that are no numbers (a warp).
+// The 8 dims from 4 d4 of a lane's vector - row `row` of the cut pair that begins in
+// row0, query head h of KV head g - where the merge of its parts gave some that are
+// no numbers (a warp).
 struct Dims8 {
   float4 o[2];
 };
 __device__ __noinline__ Dims8 again_parts(const ChunkArgs& a, int row0, int g, int row, int h, bool ok, int d4,
                                           Dims8 was) {
+  const PagedView& kv = a.p.kv;
+  const float ninf = -__int_as_float(0x7f800000);
   int b = 0, r0 = 0, m = 0;
-  for (; b < a.p.kv.B; ++b) {  // the sequence that has the row
+  for (; b < kv.B; ++b) {  // the sequence that has the row
     m = paged_rows(a.p.row_off, a.p.n_rows, b, r0, nullptr);
     if (row0 >= r0 && row0 - r0 < m) break;
   }
-  if (b == a.p.kv.B) return was;
-  const int N = paged_tokens(a.p.kv, b, nullptr);
-  const bool odd = odd_values(a, b, g, pair_geom(a, N, m, (row0 - r0) / (2 * a.R)));
-  const unsigned dims = __ballot_sync(0xffffffffu, odd) & (3u << d4);
-  if (!dims) return was;
+  if (b == kv.B) return was;
+  const int N = paged_tokens(kv, b, nullptr), lane = threadIdx.x & 31;
+  const Geom q = pair_geom(a, N, m, (row0 - r0) / (2 * a.R));
+  const int p = q.p0 + row;
+  if (!(__ballot_sync(0xffffffffu, dims_to_take(a, b, g, q, -1) != 0u) & (3u << d4))) return was;  // (no value at all)
+  uint32_t take = 0u;  // this lane's groups of 4 dims
   for (unsigned todo = __ballot_sync(0xffffffffu, ok); todo; todo &= todo - 1) {
     const int from = __ffs(todo) - 1;
-    const int i = row0 - r0 + __shfl_sync(0xffffffffu, row, from);
-    const float4 y = again_vector(a, b, r0 + i, N - m + i, __shfl_sync(0xffffffffu, h, from));
-    for (int x = 0; x < 2; ++x) {
-      const float4 mine = make_float4(__shfl_sync(0xffffffffu, y.x, d4 + x), __shfl_sync(0xffffffffu, y.y, d4 + x),
-                                      __shfl_sync(0xffffffffu, y.z, d4 + x), __shfl_sync(0xffffffffu, y.w, d4 + x));
-      if ((threadIdx.x & 31) == from && (dims >> (d4 + x) & 1u)) was.o[x] = mine;
+    const unsigned dims =
+        __ballot_sync(0xffffffffu, dims_to_take(a, b, g, q, __shfl_sync(0xffffffffu, p, from)) != 0u);
+    if (lane == from) take = (dims >> d4) & 3u;
+  }
+  if (!__any_sync(0xffffffffu, take != 0u)) return was;
+  // a lane has a vector: its query comes 8 dims at a time, keys and values are the same for all
+  const uint4* qr = reinterpret_cast<const uint4*>(a.p.q + (size_t)(row0 + (ok ? row : 0)) * a.p.q_row_stride +
+                                                   (size_t)(ok ? h : g * a.p.G) * kHeadDim);
+  const int first = min(q.S, q.lo), all = first + q.p1 + 1 - q.lo;
+  float mx = ninf, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int x0 = 0; x0 < all; x0 += 4) {
+    long long at[4];
+    bool see[4];
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = x0 + u, t = x < first ? x : q.lo + x - first, e = t / kv.page_size;
+      const int page = x < all ? __ldg(kv.table + (size_t)b * kv.max_pages + e) : -1;
+      see[u] = page >= 0 && page < kv.n_pages;
+      at[u] = paged_offset(kv, see[u] ? page : 0, g, see[u] ? t - e * kv.page_size : 0);
+      see[u] = see[u] && t <= p && (!a.p.window || t > p - a.p.window || t < a.p.sinks);
+    }
+#pragma unroll 1
+    for (int c = 0; c < 16; ++c) {
+      const uint4 qw = __ldg(qr + c);
+      const uint32_t qv[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint4 kw = __ldg(reinterpret_cast<const uint4*>(kv.k + at[u]) + c);
+        const uint32_t kx[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+        for (int d = 0; d < 4; ++d) z[u] += bf16_lo(qv[d]) * bf16_lo(kx[d]) + bf16_hi(qv[d]) * bf16_hi(kx[d]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(kv.v + at[u] + 8 * d4));
+      const uint32_t vv[4] = {vw.x, vw.y, vw.z, vw.w};
+      next_token<8>(see[u] ? z[u] * a.scale_log2 : ninf, vv, mx, l, o);
     }
   }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (take >> x & 1u) was.o[x] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
   return was;
 }
 
@@ -1225,10 +1303,10 @@ __device__ __noinline__ void again_rows(const ChunkArgs& a, int ctas) {
       bool cut = false;
       for (int c = lane; c < ctas; c += 32) cut |= a.recs[c].rows > 0 && a.recs[c].row0 == r0 + 2 * a.R * j && a.recs[c].g == g;
       if (__any_sync(0xffffffffu, cut)) continue;  // again_parts
-      const bool odd = odd_values(a, b, g, pair_geom(a, N, m, j));
-      if (!__any_sync(0xffffffffu, odd)) continue;
+      const uint32_t dims = dims_to_take(a, b, g, pair_geom(a, N, m, j), N - m + i);
+      if (!__any_sync(0xffffffffu, dims != 0u)) continue;
       o = again_vector(a, b, r0 + i, N - m + i, h);
-      if (!odd) continue;  // (the other dims stay as they are)
+      if (!dims) continue;  // (the other dims stay as they are)
       if (a.p.out)
         *reinterpret_cast<float4*>(a.p.out + at) = o;
       else

@@ -494,9 +494,9 @@ sa_status sparse_attn_cache_read(const sa_paged_desc* kv, int32_t first_token, v
  * included; a NaN in q, or in a bf16 key that a row sees, makes that row NaN;
  * a NaN or infinity in a bf16 value that a row sees makes its dim of the row
  * NaN or infinite.  Rows that do not see it are not touched (the dims around
- * such a value are then computed again one by one, which is slow).  A NaN code
- * of an e4m3 row that is seen, and infinities in q or keys, give undefined
- * results.  Any m_b from 0 on; lengths are read on the device only, so a
+ * such a value are then computed again, which can take 50 times as long).
+ * A NaN code of an e4m3 row that is seen, and infinities in q or keys, give
+ * undefined results.  Any m_b from 0 on; lengths are read on the device only, so a
  * captured call replays with other lengths.  Two launches. */
 sa_status sparse_attn_chunk(const sa_paged_desc* kv, const void* q, int64_t q_row_stride,
                             int32_t n_q_heads, const int32_t* row_off, int32_t n_rows,

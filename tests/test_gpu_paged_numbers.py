@@ -400,3 +400,24 @@ def test_a_nan_value_in_the_single_token_form(cuda_dev, sa, out, window, sinks):
     lost[0, 4:, [100, 50] + ([] if window else [9])] = True
     assert torch.isnan(got[0][lost]).all()
     assert torch.equal(got[0][~lost], want[0][~lost]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,rows,window,sinks", ODD[:4])
+@pytest.mark.parametrize("which", ["last", "all"])
+def test_whole_value_rows_of_no_numbers(cuda_dev, sa, out, lens, rows, window, sinks, which):
+    """All dims of the newest token's value: the newest row alone loses its
+    output; of all new tokens' values: every row does.  lse is as it was."""
+    c = Case(sa, cuda_dev, lens=lens, rows=rows, hq=8, hkv=2, page=16, cache="bf16", out=out, seed=211, gaps=2)
+    want = c.run(window, sinks)
+    lost = torch.zeros(c.n_rows, dtype=torch.bool)
+    for b, (N, m) in enumerate(zip(lens, rows)):
+        for t in range(N - 1 if which == "last" else N - m, N):
+            c.dv[int(c.table[b, t // 16]), :, t % 16] = float("nan")
+            lost[c.off[b] + t - (N - m)] = True
+    got = c.run(window, sinks)
+    assert c.status() == sa.SA_OK
+    assert torch.isnan(got[0][lost]).all()
+    got[0][lost] = want[0][lost]
+    c.check(got, window, sinks)
+    assert torch.equal(got[1], want[1])
